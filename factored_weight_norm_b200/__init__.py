@@ -9,9 +9,13 @@ layer's norm needs.
 from .dora import (  # noqa: F401
     DoraError,
     dora_compose_bwd,
+    dora_compose_bwd_ckpt8,
+    dora_compose_bwd_ckpt8_workspace_size,
     dora_compose_bwd_noalloc,
     dora_compose_bwd_workspace_size,
     dora_compose_fwd,
+    dora_compose_fwd_ckpt8,
+    dora_dequantize_i8,
     dora_device_status,
     dora_factored_norm,
     dora_factored_norm_batched,
@@ -21,9 +25,14 @@ from .dora import (  # noqa: F401
     dora_factored_norm_sq,
     dora_factored_norm_workspace_size,
     dora_fused_linear_fwd,
+    dora_fused_linear_fwd_ckpt8,
     dora_fused_linear_fwd_workspace_size,
     dora_launch_count,
+    dora_linear_i8_fwd,
+    dora_linear_i8_fwd_workspace_size,
     dora_norm_finish,
     dora_num_sms,
+    dora_quantize_rows_i8,
+    dora_rms_norm_i8,
     dora_status_string,
 )

@@ -1,0 +1,305 @@
+// ckpt8.cuh - the compose forward that keeps its backward's input in 8 bits,
+// and the backward that reads it.
+//
+// The compose backward needs the two activations only through
+//   z = (base - b) + s * lora,   d_m = (sum_t dy * z) / n,
+// so the forward keeps z alone, as int8 codes with one fp32 scale per token
+// and 128 columns (quant8.cuh): 1.03 bytes an element instead of the 4 (bf16)
+// or 8 (fp32) of base and lora.  A code is off by at most half its scale,
+// top / 254; d_m sums many of them, d_base and d_lora do not depend on z.
+//
+// z is formed as fp32 (base - b) + (s * lora) with each operation rounded, so
+// that the codes are those of the same expression anywhere else; y is
+// compose_fwd_kernel's expression, bit for bit.
+//
+// Both kernels are bound by memory (bf16: 7.03 bytes an element each).  A
+// group of lanes owns the 128 columns of a scale, so that their maximum is one
+// warp reduction: 16 lanes of 8 bf16 (two groups a warp), or 32 lanes of 4
+// fp32, neighbours where rows are whole 16-byte vectors, else 32 columns
+// apart (4-byte accesses, still coalesced).
+#pragma once
+
+#include "quant8.cuh"
+
+namespace dora {
+
+// How the lanes of a warp cover a row's 128-column blocks.
+struct LanesBf16 {
+  using T = __nv_bfloat16;
+  using Raw = uint4;
+  static constexpr int kE = 8, kLanes = 16;
+  static __device__ __forceinline__ int col(int gl, int e) { return gl * 8 + e; }
+  static __device__ __forceinline__ bool any(int gl, long long left) { return gl * 8 < left; }
+  static __device__ __forceinline__ Raw load(const T* p, int gl, long long) { return ld_stream_u4(p + gl * 8); }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[8]) { VecIO<T, 8>::unpack(r, v); }
+  static __device__ __forceinline__ void store(T* p, int gl, long long, const float (&v)[8]) {
+    VecIO<T, 8>::store(p + gl * 8, v);
+  }
+  using Codes = uint2;
+  static __device__ __forceinline__ Codes load_codes(const int8_t* p, int gl, long long) {
+    return ld_stream_u2(p + gl * 8);
+  }
+  static __device__ __forceinline__ void unpack_code(const Codes& c, float (&v)[8]) {
+    float lo[4], hi[4];
+    unpack_codes(c.x, lo);
+    unpack_codes(c.y, hi);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = lo[e];
+      v[4 + e] = hi[e];
+    }
+  }
+  static __device__ __forceinline__ void store_codes(int8_t* p, int gl, long long, const uint32_t (&q)[8]) {
+    CodeIO<8>::store(p + gl * 8, q);
+  }
+};
+
+struct LanesF32 {
+  using T = float;
+  using Raw = uint4;
+  static constexpr int kE = 4, kLanes = 32;
+  static __device__ __forceinline__ int col(int gl, int e) { return gl * 4 + e; }
+  static __device__ __forceinline__ bool any(int gl, long long left) { return gl * 4 < left; }
+  static __device__ __forceinline__ Raw load(const T* p, int gl, long long) { return ld_stream_u4(p + gl * 4); }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[4]) { VecIO<T, 4>::unpack(r, v); }
+  static __device__ __forceinline__ void store(T* p, int gl, long long, const float (&v)[4]) {
+    VecIO<T, 4>::store(p + gl * 4, v);
+  }
+  using Codes = uint32_t;
+  static __device__ __forceinline__ Codes load_codes(const int8_t* p, int gl, long long) {
+    return ld_stream_u1(p + gl * 4);
+  }
+  static __device__ __forceinline__ void unpack_code(const Codes& c, float (&v)[4]) { unpack_codes(c, v); }
+  static __device__ __forceinline__ void store_codes(int8_t* p, int gl, long long, const uint32_t (&q)[4]) {
+    CodeIO<4>::store(p + gl * 4, q);
+  }
+};
+
+// Any width and 4-byte alignment: columns gl, gl + 32, gl + 64, gl + 96.
+struct LanesF32Any {
+  using T = float;
+  struct Raw {
+    float v[4];
+  };
+  static constexpr int kE = 4, kLanes = 32;
+  static __device__ __forceinline__ int col(int gl, int e) { return gl + 32 * e; }
+  static __device__ __forceinline__ bool any(int gl, long long left) { return gl < left; }
+  static __device__ __forceinline__ Raw load(const T* p, int gl, long long left) {
+    Raw r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r.v[e] = gl + 32 * e < left ? __ldg(p + gl + 32 * e) : 0.f;
+    return r;
+  }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = r.v[e];
+  }
+  static __device__ __forceinline__ void store(T* p, int gl, long long left, const float (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (gl + 32 * e < left) p[gl + 32 * e] = v[e];
+  }
+  struct Codes {
+    int8_t q[4];
+  };
+  static __device__ __forceinline__ Codes load_codes(const int8_t* p, int gl, long long left) {
+    Codes c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c.q[e] = gl + 32 * e < left ? __ldg(p + gl + 32 * e) : static_cast<int8_t>(0);
+    return c;
+  }
+  static __device__ __forceinline__ void unpack_code(const Codes& c, float (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(c.q[e]);
+  }
+  static __device__ __forceinline__ void store_codes(int8_t* p, int gl, long long left, const uint32_t (&q)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (gl + 32 * e < left) p[gl + 32 * e] = static_cast<int8_t>(q[e]);
+  }
+};
+
+// Maximum over the lanes of a group (the lanes of `mask`).
+template <int LANES>
+__device__ __forceinline__ uint32_t group_max(uint32_t mask, uint32_t v) {
+  if constexpr (LANES == 32) {
+    return __reduce_max_sync(mask, v);
+  } else {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(mask, v, o));
+    return v;
+  }
+}
+
+// ------------------------------------------------------------------ forward
+constexpr int kCkptRows = 4;  // rows in flight per thread
+
+template <typename L>
+__global__ void __launch_bounds__(256) compose_fwd_ckpt8_kernel(
+    const typename L::T* __restrict__ base, const typename L::T* __restrict__ lora,
+    const typename L::T* __restrict__ bias, const float* __restrict__ m, const float* __restrict__ n, float s,
+    long long tokens, long long d_out, long long blocks, typename L::T* __restrict__ y, int8_t* __restrict__ z8,
+    float* __restrict__ z_scale, long long rows_per_cta) {
+  using T = typename L::T;
+  constexpr int E = L::kE;
+  const int gl = threadIdx.x % L::kLanes;
+  const long long block = blockIdx.x * static_cast<long long>(blockDim.x / L::kLanes) + threadIdx.x / L::kLanes;
+  const uint32_t group = L::kLanes == 32 ? 0xFFFFFFFFu : 0xFFFFu << (threadIdx.x & 16);
+  if (block >= blocks) return;  // a whole group of lanes
+  const long long col0 = block * kCkptBlock;
+  const long long left = d_out - col0;
+  const bool any = L::any(gl, left);
+  float delta[E], gs[E], bb[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = L::col(gl, e);
+    const bool ok = c < left;
+    const float mm = ok ? __ldg(m + col0 + c) : 1.f, nn = ok ? __ldg(n + col0 + c) : 1.f;
+    delta[e] = (mm - nn) / nn;
+    gs[e] = (mm / nn) * s;
+    bb[e] = ok && bias ? ld_param(bias + col0 + c) : 0.f;
+  }
+  const long long row0 = blockIdx.y * rows_per_cta;
+  const long long row1 = min(tokens, row0 + rows_per_cta);
+  for (long long row = row0; row < row1; row += kCkptRows) {
+    typename L::Raw rb[kCkptRows], rl[kCkptRows];
+#pragma unroll
+    for (int k = 0; k < kCkptRows; ++k) {
+      rb[k] = typename L::Raw{};
+      rl[k] = typename L::Raw{};
+      if (any && row + k < row1) {
+        rb[k] = L::load(base + (row + k) * d_out + col0, gl, left);
+        rl[k] = L::load(lora + (row + k) * d_out + col0, gl, left);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kCkptRows; ++k) {
+      if (row + k < row1) {  // the same for the whole group
+        float b[E], l[E], o[E], z[E];
+        uint32_t q[E], top = 0;
+        L::unpack(rb[k], b);
+        L::unpack(rl[k], l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float inner = b[e] - bb[e];
+          o[e] = b[e] + fmaf(delta[e], inner, gs[e] * l[e]);
+          z[e] = __fadd_rn(inner, __fmul_rn(s, l[e]));
+          top = max(top, abs_bits(z[e]));
+        }
+        top = group_max<L::kLanes>(group, top);
+        codes_of<E>(z, top, top_inverse(top), q);
+        if (any) {
+          L::store(y + (row + k) * d_out + col0, gl, left, o);
+          L::store_codes(z8 + (row + k) * d_out + col0, gl, left, q);
+        }
+        if (gl == 0) z_scale[(row + k) * blocks + block] = top_scale(top);
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- backward
+// compose_bwd_kernel's schedule (compose.cuh) with z read from the codes: a
+// CTA takes one 128-column strip of a chunk of rows, each thread carries its
+// columns' sums in fp32, and the last CTA of a strip adds the chunks in order.
+constexpr int kCkptBwdThreads = 256;
+constexpr int kCkptBwdRows = 4;  // rows in flight per thread
+
+template <typename L>
+__global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
+    const typename L::T* __restrict__ dy, const int8_t* __restrict__ z8, const float* __restrict__ z_scale,
+    const float* __restrict__ m, const float* __restrict__ n, float s, long long tokens, long long d_out,
+    long long blocks, typename L::T* __restrict__ d_base, typename L::T* __restrict__ d_lora,
+    float* __restrict__ partial, unsigned long long* __restrict__ counters, float* __restrict__ d_m,
+    long long rows_per_chunk, unsigned long long epoch) {
+  constexpr int E = L::kE;
+  constexpr int kSlots = kCkptBwdThreads / L::kLanes;  // rows visited at once
+  __shared__ float red[kSlots][kCkptBlock];
+  __shared__ int is_last;
+  const int gl = threadIdx.x % L::kLanes, slot = threadIdx.x / L::kLanes;
+  const long long block = blockIdx.x;
+  const long long col0 = block * kCkptBlock;
+  const long long left = d_out - col0;
+  float g[E], acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = L::col(gl, e);
+    g[e] = c < left ? __ldg(m + col0 + c) / __ldg(n + col0 + c) : 0.f;
+    acc[e] = 0.f;
+  }
+  if (L::any(gl, left)) {
+    const long long row0 = blockIdx.y * rows_per_chunk;
+    const long long row1 = min(tokens, row0 + rows_per_chunk);
+    for (long long row = row0 + slot; row < row1; row += kCkptBwdRows * kSlots) {
+      typename L::Raw ra[kCkptBwdRows];
+      typename L::Codes rz[kCkptBwdRows];
+      float sc[kCkptBwdRows];
+#pragma unroll
+      for (int u = 0; u < kCkptBwdRows; ++u) {
+        const long long rr = row + u * kSlots;
+        if (rr < row1) {
+          ra[u] = L::load(dy + rr * d_out + col0, gl, left);
+          rz[u] = L::load_codes(z8 + rr * d_out + col0, gl, left);
+          sc[u] = __ldg(z_scale + rr * blocks + block);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kCkptBwdRows; ++u) {
+        const long long rr = row + u * kSlots;
+        if (rr < row1) {
+          float a[E], z[E], db[E], dl[E];
+          L::unpack(ra[u], a);
+          L::unpack_code(rz[u], z);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            db[e] = g[e] * a[e];
+            dl[e] = s * db[e];
+            acc[e] = fmaf(a[e], z[e] * sc[u], acc[e]);
+          }
+          L::store(d_base + rr * d_out + col0, gl, left, db);
+          L::store(d_lora + rr * d_out + col0, gl, left, dl);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) red[slot][L::col(gl, e)] = acc[e];
+  __syncthreads();
+  const int t = threadIdx.x;
+  const bool t_ok = t < kCkptBlock && t < left;
+  if (t_ok) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSlots; ++w) sum += red[w][t];
+    partial[blockIdx.y * d_out + col0 + t] = sum;
+  }
+  __threadfence();
+  __syncthreads();
+  // arrivals tagged with this call's epoch, as in compose_bwd_kernel: a word
+  // with another tag counts as zero, so nothing is cleared before the launch
+  const unsigned long long tag = epoch << 8;
+  if (t == 0) {
+    unsigned long long* c = counters + block;
+    unsigned long long v = *reinterpret_cast<volatile unsigned long long*>(c);
+    int seen = 0;
+    while (true) {
+      seen = (v & ~0xffull) == tag ? static_cast<int>(v & 0xffull) : 0;
+      const unsigned long long prev = atomicCAS(c, v, tag | static_cast<unsigned long long>(seen + 1));
+      if (prev == v) break;
+      v = prev;
+    }
+    is_last = (seen == static_cast<int>(gridDim.y) - 1);
+  }
+  __syncthreads();
+  if (is_last) {
+    __threadfence();
+    if (t_ok) {
+      float total = 0.f;
+      for (unsigned c = 0; c < gridDim.y; ++c) total += ld_cg_f32(&partial[c * d_out + col0 + t]);
+      d_m[col0 + t] = total / __ldg(n + col0 + t);
+    }
+    if (t == 0) counters[block] = tag;  // count 0 under this tag: a replay of the same launch starts clean
+  }
+}
+
+}  // namespace dora

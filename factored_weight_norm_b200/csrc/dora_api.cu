@@ -18,7 +18,9 @@
 #include <mutex>
 
 #include "../../include/dora.h"
+#include "ckpt8.cuh"
 #include "compose.cuh"
+#include "linear_i8.cuh"
 #include "linear_tc.cuh"
 #include "norm_bwd.cuh"
 #include "norm_simt.cuh"
@@ -57,6 +59,15 @@ int pick_bn(long long N) {
     }
   }
   return best;
+}
+
+// linear_i8_pair_kernel: the same stages beside its column factors
+int linear_i8_stages(int smem_optin) {
+  return static_cast<int>(
+      std::min<size_t>(kLinStagesMax, (smem_optin - 1024 - kI8ColBytes - kI8BarrierBytes) / kPairStageBytes));
+}
+size_t linear_i8_smem(int smem_optin) {
+  return static_cast<size_t>(linear_i8_stages(smem_optin)) * kPairStageBytes + 1024 + kI8ColBytes + kI8BarrierBytes;
 }
 
 template <typename K>
@@ -145,7 +156,9 @@ int device_info(DeviceInfo** out) {
       return DORA_ERR_CUDA;
     if (pair_attrs(linear_pair_kernel<false, false>, d.smem_optin) ||
         pair_attrs(linear_pair_kernel<false, true>, d.smem_optin) ||
-        pair_attrs(linear_pair_kernel<true, true>, d.smem_optin))
+        pair_attrs(linear_pair_kernel<true, true>, d.smem_optin) ||
+        pair_attrs(linear_pair_kernel<false, false, true>, d.smem_optin) ||
+        pair_attrs(linear_i8_pair_kernel, d.smem_optin))
       return DORA_ERR_CUDA;
     {
       cudaLaunchConfig_t occ{};
@@ -186,6 +199,19 @@ int make_map(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, ui
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
                               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DORA_OK : DORA_ERR_CUDA;
+}
+
+// 2-D int8 tensor map over a row-major [rows, cols] matrix, 128 x box_rows
+// boxes, 128-byte swizzle, zero fill outside the matrix.
+int make_map_i8(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kI8BK), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? DORA_OK : DORA_ERR_CUDA;
 }
@@ -845,9 +871,65 @@ size_t dora_fused_linear_fwd_workspace_size(int64_t tokens, int64_t r) {
   return std::max<size_t>(256, align_up(static_cast<size_t>(tokens) * static_cast<size_t>(r) * 2, 256));
 }
 
-int dora_fused_linear_fwd(const void* x, const void* W, const void* A, const void* B, const void* bias, const float* m,
-                          const float* n, float s, int64_t tokens, int64_t d_in, int64_t d_out, int64_t r,
-                          dora_dtype dt, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+}  // extern "C"
+
+namespace dora {
+namespace {
+
+// Launch configuration of a CTA-pair kernel over `tiles` output tiles: as many
+// pairs as are resident at once.  `after`: it starts under the launch before it
+// (programmatic dependent launch) and waits itself for what it reads of that.
+cudaLaunchConfig_t pair_config(cudaLaunchAttribute (&attrs)[2], int threads, size_t smem, long long tiles, bool after,
+                               const DeviceInfo* dev, cudaStream_t st) {
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = 2;
+  attrs[0].val.clusterDim.y = 1;
+  attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  cfg.attrs = attrs;
+  cfg.numAttrs = after ? 2 : 1;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<long long>(dev->pair_clusters, tiles)));
+  return cfg;
+}
+
+// P = bf16(s * x A^T) into `P` [tokens, r]; ordered after everything before it
+// on the stream.  tmA has boxes of pick_bn(r) / 2 rows.
+int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, float s, int64_t tokens, int64_t d_in,
+             int64_t r, const DeviceInfo* dev, cudaStream_t st) {
+  LinearArgs pa{};
+  pa.M = static_cast<int>(tokens);
+  pa.N = static_cast<int>(r);
+  pa.kb_main = pa.kb_total = static_cast<int>(cdiv(d_in, kLinBK));
+  pa.tiles_m = static_cast<int>(cdiv(tokens, kPairBM));
+  pa.bn = pick_bn(r);
+  pa.tiles_n = static_cast<int>(cdiv(r, pa.bn));
+  pa.stages = linear_pair_stages(dev->smem_optin);
+  pa.alpha = s;
+  pa.out = P;
+  pa.ldo = r;
+  pa.wait_limit = kWaitLimitCycles;
+  pa.status = dev->status;
+  cudaLaunchAttribute attrs[2];
+  cudaLaunchConfig_t cfg = pair_config(attrs, kLinThreads, linear_pair_smem(dev->smem_optin),
+                                       static_cast<long long>(pa.tiles_m) * pa.tiles_n, false, dev, st);
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<false, false>, tmX, tmA, tmX, tmA, pa) == cudaSuccess
+             ? DORA_OK
+             : DORA_ERR_CUDA;
+}
+
+// Tile width of a linear that keeps codes: a tile holds whole 128-column stretches.
+int pick_bn_ckpt(long long N) { return N <= kCkptBlock ? kCkptBlock : 256; }
+
+int fused_linear(const void* x, const void* W, const void* A, const void* B, const void* bias, const float* m,
+                 const float* n, float s, int64_t tokens, int64_t d_in, int64_t d_out, int64_t r, dora_dtype dt,
+                 void* y, bool ckpt, int8_t* z8, float* z_scale, void* workspace, size_t workspace_bytes,
+                 void* stream) {
   if (dt != DORA_BF16) return DORA_ERR_UNSUPPORTED;
   if (tokens < 0 || d_in < 0 || d_out < 0 || r < 0) return DORA_ERR_INVALID_ARG;
   if (tokens == 0 || d_out == 0) return DORA_OK;
@@ -855,9 +937,10 @@ int dora_fused_linear_fwd(const void* x, const void* W, const void* A, const voi
   if (tokens > INT32_MAX / 2 || d_in > INT32_MAX / 2 || d_out > INT32_MAX / 2 || r > INT32_MAX / 2)
     return DORA_ERR_UNSUPPORTED;
   if (!x || !W || !m || !n || !y || (r > 0 && (!A || !B))) return DORA_ERR_INVALID_ARG;
+  if (ckpt && (!z8 || !z_scale)) return DORA_ERR_INVALID_ARG;
   if (d_in % 8 != 0 || d_out % 8 != 0 || r % 8 != 0) return DORA_ERR_UNSUPPORTED;
   if (!aligned(x, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(y, 16) ||
-      !aligned(bias, 2) || !aligned(m, 4) || !aligned(n, 4))
+      !aligned(bias, 2) || !aligned(m, 4) || !aligned(n, 4) || !aligned(z8, 16) || !aligned(z_scale, 4))
     return DORA_ERR_UNSUPPORTED;
   if (cdiv(tokens, kPairBM) * cdiv(d_out, 128) > INT32_MAX) return DORA_ERR_UNSUPPORTED;
   const size_t need = dora_fused_linear_fwd_workspace_size(tokens, r);
@@ -869,7 +952,7 @@ int dora_fused_linear_fwd(const void* x, const void* W, const void* A, const voi
   __nv_bfloat16* P = static_cast<__nv_bfloat16*>(workspace);
 
   // B-side boxes hold the bn / 2 rows one CTA of a pair owns
-  const int bn_p = r > 0 ? pick_bn(r) : 256, bn_y = pick_bn(d_out);
+  const int bn_p = r > 0 ? pick_bn(r) : 256, bn_y = ckpt ? pick_bn_ckpt(d_out) : pick_bn(d_out);
   CUtensorMap tmX, tmW, tmA, tmP, tmB;
   if (make_map(&tmX, x, tokens, d_in) || make_map(&tmW, W, d_out, d_in, bn_y / 2)) return DORA_ERR_CUDA;
   if (r > 0 && (make_map(&tmA, A, r, d_in, bn_p / 2) || make_map(&tmP, P, tokens, r) ||
@@ -879,44 +962,7 @@ int dora_fused_linear_fwd(const void* x, const void* W, const void* A, const voi
   const int stages = linear_pair_stages(dev->smem_optin);
   if (stages < 2) return DORA_ERR_UNSUPPORTED;
   const long long tiles_m2 = cdiv(tokens, kPairBM);
-
-  cudaLaunchAttribute attrs[2];
-  attrs[0].id = cudaLaunchAttributeClusterDimension;
-  attrs[0].val.clusterDim.x = 2;
-  attrs[0].val.clusterDim.y = 1;
-  attrs[0].val.clusterDim.z = 1;
-  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attrs[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.stream = st;
-  cfg.attrs = attrs;
-  cfg.blockDim = dim3(kLinThreads);
-  cfg.dynamicSmemBytes = linear_pair_smem(dev->smem_optin);
-  auto pairs_for = [&](long long tiles) {
-    return static_cast<unsigned>(2 * std::min<long long>(dev->pair_clusters, tiles));
-  };
-
-  // 1) P = bf16(s * x A^T) into the workspace
-  if (r > 0) {
-    LinearArgs pa{};
-    pa.M = static_cast<int>(tokens);
-    pa.N = static_cast<int>(r);
-    pa.kb_main = pa.kb_total = kb_main;
-    pa.tiles_m = static_cast<int>(tiles_m2);
-    pa.bn = bn_p;
-    pa.tiles_n = static_cast<int>(cdiv(r, bn_p));
-    pa.stages = stages;
-      pa.alpha = s;
-    pa.out = P;
-    pa.ldo = r;
-    pa.wait_limit = kWaitLimitCycles;
-    pa.status = dev->status;
-    cfg.numAttrs = 1;  // cluster shape only: ordered after everything before it on the stream
-    cfg.gridDim = dim3(pairs_for(static_cast<long long>(pa.tiles_m) * pa.tiles_n));
-    note_launch();
-    if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<false, false>, tmX, tmA, tmX, tmA, pa) != cudaSuccess)
-      return DORA_ERR_CUDA;
-  }
+  if (r > 0 && launch_p(tmX, tmA, P, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
 
   // 2) y = bf16(g * [x | P] [W | B]^T + b), dependent on 1) only for the extension blocks
   LinearArgs la{};
@@ -934,19 +980,319 @@ int dora_fused_linear_fwd(const void* x, const void* W, const void* A, const voi
   la.bias = static_cast<const __nv_bfloat16*>(bias);
   la.out = static_cast<__nv_bfloat16*>(y);
   la.ldo = d_out;
+  la.z8 = z8;
+  la.z_scale = z_scale;
   la.ext_waits = r > 0 ? 1 : 0;
   la.wait_limit = kWaitLimitCycles;
   la.status = dev->status;
-  cfg.numAttrs = r > 0 ? 2 : 1;
-  cfg.gridDim = dim3(pairs_for(static_cast<long long>(la.tiles_m) * la.tiles_n));
+  cudaLaunchAttribute attrs[2];
+  cudaLaunchConfig_t cfg = pair_config(attrs, kLinThreads, linear_pair_smem(dev->smem_optin),
+                                       static_cast<long long>(la.tiles_m) * la.tiles_n, r > 0, dev, st);
   const CUtensorMap& tmA2 = r > 0 ? tmP : tmX;
   const CUtensorMap& tmB2 = r > 0 ? tmB : tmW;
   note_launch();
-  if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<false, false>, tmX, tmW, tmA2, tmB2, la) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, ckpt ? linear_pair_kernel<false, false, true> : linear_pair_kernel<false, false>, tmX,
+                         tmW, tmA2, tmB2, la) != cudaSuccess)
     return DORA_ERR_CUDA;
   return launch_error();
 }
 
+}  // namespace
+}  // namespace dora
+
+extern "C" {
+
+int dora_fused_linear_fwd(const void* x, const void* W, const void* A, const void* B, const void* bias, const float* m,
+                          const float* n, float s, int64_t tokens, int64_t d_in, int64_t d_out, int64_t r,
+                          dora_dtype dt, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  return fused_linear(x, W, A, B, bias, m, n, s, tokens, d_in, d_out, r, dt, y, false, nullptr, nullptr, workspace,
+                      workspace_bytes, stream);
+}
+
+int dora_fused_linear_fwd_ckpt8(const void* x, const void* W, const void* A, const void* B, const void* bias,
+                                const float* m, const float* n, float s, int64_t tokens, int64_t d_in, int64_t d_out,
+                                int64_t r, dora_dtype dt, void* y, int8_t* z8, float* z_scale, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  return fused_linear(x, W, A, B, bias, m, n, s, tokens, d_in, d_out, r, dt, y, true, z8, z_scale, workspace,
+                      workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------ 8-bit operators
+}  // extern "C"
+
+namespace dora {
+namespace {
+
+// Rows to codes: the smallest number of columns per thread (8, 16 or 32) that
+// covers a row with `most` threads.  Few rows take many threads each, so that
+// one row's latency is short; many rows take 256, so that several CTAs are
+// resident and one's reduction overlaps another's loads.
+template <typename T, int VEC>
+int launch_rows_i8(const RowsI8Args& a, const DeviceInfo* dev, cudaStream_t st) {
+  const long long most = a.rows < 2LL * dev->num_sms ? 1024 : 256;
+  const unsigned grid = static_cast<unsigned>(a.rows);
+  const long long vecs = cdiv(a.d, VEC);
+  note_launch();
+  const auto threads = [&](long long nv) { return static_cast<unsigned>(align_up(cdiv(vecs, nv), 32)); };
+  if (cdiv(a.d, 8) <= most)
+    rows_i8_kernel<T, VEC, 8 / VEC><<<grid, threads(8 / VEC), 0, st>>>(a);
+  else if (cdiv(a.d, 16) <= most)
+    rows_i8_kernel<T, VEC, 16 / VEC><<<grid, threads(16 / VEC), 0, st>>>(a);
+  else if (cdiv(a.d, 32) <= 1024)
+    rows_i8_kernel<T, VEC, 32 / VEC><<<grid, threads(32 / VEC), 0, st>>>(a);
+  else
+    rows_i8_long_kernel<T, VEC><<<grid, 1024, 0, st>>>(a);
+  return launch_error();
+}
+
+int rows_i8(const void* x, const void* residual, const void* weight, bool norm, float eps, int64_t rows, int64_t d,
+            dora_dtype dt, void* h, void* y, int8_t* q, float* scale, void* stream) {
+  if (dt != DORA_BF16 && dt != DORA_F32) return DORA_ERR_UNSUPPORTED;
+  if (rows < 0 || d < 0) return DORA_ERR_INVALID_ARG;
+  if (rows == 0) return DORA_OK;
+  if (d == 0) return DORA_ERR_UNSUPPORTED;
+  if (!x || !q || !scale || (norm && !weight) || (residual && !h)) return DORA_ERR_INVALID_ARG;
+  if (norm && !(eps >= 0.f)) return DORA_ERR_INVALID_ARG;
+  if (rows > INT32_MAX || d > INT32_MAX) return DORA_ERR_UNSUPPORTED;
+  const auto all_aligned = [&](size_t e) {
+    return aligned(x, e) && aligned(residual, e) && aligned(weight, e) && (!residual || aligned(h, e)) && aligned(y, e);
+  };
+  if (dt == DORA_BF16 && (d % 8 != 0 || !all_aligned(16) || !aligned(q, 8))) return DORA_ERR_UNSUPPORTED;
+  if (!all_aligned(4) || !aligned(scale, 4)) return DORA_ERR_UNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev)) return DORA_ERR_CUDA;
+  RowsI8Args a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = norm ? weight : nullptr;
+  a.h = h;
+  a.y = y;
+  a.q = q;
+  a.scale = scale;
+  a.rows = rows;
+  a.d = d;
+  a.eps = eps;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dt == DORA_BF16) return launch_rows_i8<__nv_bfloat16, 8>(a, dev, st);
+  if (d % 4 == 0 && all_aligned(16) && aligned(q, 4)) return launch_rows_i8<float, 4>(a, dev, st);
+  return launch_rows_i8<float, 1>(a, dev, st);
+}
+
+template <typename L>
+void launch_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const void* bias, const float* m,
+                              const float* n, float s, int64_t tokens, int64_t d_out, void* y, int8_t* z8,
+                              float* z_scale, const DeviceInfo* dev, cudaStream_t st) {
+  using T = typename L::T;
+  const long long blocks = cdiv(d_out, kCkptBlock);
+  const int threads = static_cast<int>(std::min<long long>(256, align_up(blocks * L::kLanes, 32)));
+  const long long gx = cdiv(blocks, threads / L::kLanes);
+  // as compose_fwd: several short waves, about 8 CTAs per SM in total
+  const long long gy = std::max<long long>(1, std::min<long long>({8LL * dev->num_sms / gx, tokens, 65535}));
+  const long long rows = cdiv(tokens, gy);
+  note_launch();
+  compose_fwd_ckpt8_kernel<L><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(tokens, rows))), threads, 0,
+                                st>>>(static_cast<const T*>(base_out), static_cast<const T*>(lora_out),
+                                      static_cast<const T*>(bias), m, n, s, tokens, d_out, blocks,
+                                      static_cast<T*>(y), z8, z_scale, rows);
+}
+
+template <typename L>
+void launch_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_scale, const float* m, const float* n,
+                              float s, int64_t tokens, int64_t d_out, void* d_base, void* d_lora, float* d_m,
+                              uint8_t* ws, const DeviceInfo* dev, cudaStream_t st) {
+  using T = typename L::T;
+  const long long blocks = cdiv(d_out, kCkptBlock);
+  const long long slots = static_cast<long long>(dev->num_sms) * ctas_per_sm(compose_bwd_ckpt8_kernel<L>, kCkptBwdThreads);
+  const long long chunks = bwd_chunks(blocks, slots, tokens,
+                                      std::min<long long>(kMaxBwdChunks, cdiv(tokens, kCkptBwdThreads / L::kLanes)));
+  const long long rows = cdiv(tokens, chunks);
+  unsigned long long* cnt = reinterpret_cast<unsigned long long*>(ws);  // tagged: no clearing needed
+  float* part = reinterpret_cast<float*>(ws + align_up(blocks * 8, 256));
+  note_launch();
+  compose_bwd_ckpt8_kernel<L><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(cdiv(tokens, rows))),
+                                kCkptBwdThreads, 0, st>>>(
+      static_cast<const T*>(dy), z8, z_scale, m, n, s, tokens, d_out, blocks, static_cast<T*>(d_base),
+      static_cast<T*>(d_lora), part, cnt, d_m, rows, next_bwd_epoch());
+}
+
+}  // namespace
+}  // namespace dora
+
+extern "C" {
+
+int dora_rms_norm_i8(const void* x, const void* residual, const void* weight, float eps, int64_t tokens, int64_t d,
+                     dora_dtype dt, void* h, void* y, int8_t* q, float* scale, void* stream) {
+  return rows_i8(x, residual, weight, true, eps, tokens, d, dt, h, y, q, scale, stream);
+}
+
+int dora_quantize_rows_i8(const void* x, const void* residual, int64_t rows, int64_t cols, dora_dtype dt, void* h,
+                          int8_t* q, float* scale, void* stream) {
+  return rows_i8(x, residual, nullptr, false, 0.f, rows, cols, dt, h, nullptr, q, scale, stream);
+}
+
+int dora_dequantize_i8(const int8_t* q, const float* scale, int64_t rows, int64_t cols, int64_t block, dora_dtype dt,
+                       void* out, void* stream) {
+  if (dt != DORA_BF16 && dt != DORA_F32) return DORA_ERR_UNSUPPORTED;
+  if (rows < 0 || cols < 0) return DORA_ERR_INVALID_ARG;
+  if (block != 0 && block != kCkptBlock) return DORA_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return DORA_OK;
+  if (!q || !scale || !out) return DORA_ERR_INVALID_ARG;
+  if (rows > INT32_MAX || cols > INT32_MAX) return DORA_ERR_UNSUPPORTED;
+  if (!aligned(out, dt == DORA_BF16 ? 2 : 4) || !aligned(scale, 4)) return DORA_ERR_UNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev)) return DORA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long width = block ? block : cols;
+  const long long blocks = cdiv(cols, width);
+  const bool wide = cols % 8 == 0 && aligned(q, 8) && aligned(out, 16);
+  const long long vecs = wide ? cols / 8 : cols;
+  const int threads = static_cast<int>(std::min<long long>(256, align_up(vecs, 32)));
+  const long long gx = cdiv(vecs, threads);
+  const dim3 grid(static_cast<unsigned>(gx),
+                  static_cast<unsigned>(std::max<long long>(1, std::min<long long>({rows, 65535, 64LL * dev->num_sms / gx}))));
+  note_launch();
+  if (dt == DORA_BF16) {
+    auto* o = static_cast<__nv_bfloat16*>(out);
+    if (wide)
+      dequant_i8_kernel<__nv_bfloat16, 8><<<grid, threads, 0, st>>>(q, scale, rows, cols, width, blocks, o);
+    else
+      dequant_i8_kernel<__nv_bfloat16, 1><<<grid, threads, 0, st>>>(q, scale, rows, cols, width, blocks, o);
+  } else {
+    auto* o = static_cast<float*>(out);
+    if (wide)
+      dequant_i8_kernel<float, 8><<<grid, threads, 0, st>>>(q, scale, rows, cols, width, blocks, o);
+    else
+      dequant_i8_kernel<float, 1><<<grid, threads, 0, st>>>(q, scale, rows, cols, width, blocks, o);
+  }
+  return launch_error();
+}
+
+size_t dora_linear_i8_fwd_workspace_size(int64_t tokens, int64_t r) {
+  return dora_fused_linear_fwd_workspace_size(tokens, r);
+}
+
+int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_q, const float* w_scale, const void* x,
+                       const void* A, const void* B, const void* bias, const float* m, const float* n, float s,
+                       int64_t tokens, int64_t d_in, int64_t d_out, int64_t r, dora_dtype dt, void* y, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (dt != DORA_BF16) return DORA_ERR_UNSUPPORTED;
+  if (tokens < 0 || d_in < 0 || d_out < 0 || r < 0) return DORA_ERR_INVALID_ARG;
+  if (tokens == 0 || d_out == 0) return DORA_OK;
+  if (!x_q || !x_scale || !W_q || !w_scale || !y || (r > 0 && (!x || !A || !B)) || ((m == nullptr) != (n == nullptr)))
+    return DORA_ERR_INVALID_ARG;
+  if (d_in == 0 || d_in % 16 != 0 || d_out % 8 != 0 || r % 8 != 0) return DORA_ERR_UNSUPPORTED;
+  // int32 holds d_in products of two codes, -128 among them: 2^14 * d_in < 2^31
+  if (d_in > kI8MaxDIn || tokens > INT32_MAX / 2 || d_out > INT32_MAX / 2 || r > INT32_MAX / 2)
+    return DORA_ERR_UNSUPPORTED;
+  if (cdiv(tokens, kPairBM) * cdiv(d_out, 128) > INT32_MAX) return DORA_ERR_UNSUPPORTED;
+  if (!aligned(x_q, 16) || !aligned(W_q, 16) || !aligned(y, 16) || !aligned(bias, 2) || !aligned(x_scale, 4) ||
+      !aligned(w_scale, 4) || !aligned(m, 4) || !aligned(n, 4))
+    return DORA_ERR_UNSUPPORTED;
+  if (r > 0 && (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16))) return DORA_ERR_UNSUPPORTED;
+  if (r > 0 && (!workspace || workspace_bytes < dora_linear_i8_fwd_workspace_size(tokens, r)))
+    return DORA_ERR_WORKSPACE;
+  if (r > 0 && !aligned(workspace, 256)) return DORA_ERR_UNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev)) return DORA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  __nv_bfloat16* P = static_cast<__nv_bfloat16*>(workspace);
+  CUtensorMap tmXq, tmWq, tmX, tmA, tmP, tmB;
+  if (make_map_i8(&tmXq, x_q, tokens, d_in, kLinBM) || make_map_i8(&tmWq, W_q, d_out, d_in, kPairBN / 2))
+    return DORA_ERR_CUDA;
+  if (r > 0) {
+    if (make_map(&tmX, x, tokens, d_in) || make_map(&tmA, A, r, d_in, pick_bn(r) / 2) || make_map(&tmP, P, tokens, r) ||
+        make_map(&tmB, B, d_out, r, kPairBN / 2))
+      return DORA_ERR_CUDA;
+    if (launch_p(tmX, tmA, P, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
+  }
+  LinearI8Args la{};
+  la.M = static_cast<int>(tokens);
+  la.N = static_cast<int>(d_out);
+  la.kb_main = static_cast<int>(cdiv(d_in, kI8BK));
+  la.kb_total = la.kb_main + static_cast<int>(cdiv(r, kLinBK));
+  la.tiles_m = static_cast<int>(cdiv(tokens, kPairBM));
+  la.tiles_n = static_cast<int>(cdiv(d_out, kPairBN));
+  la.stages = linear_i8_stages(dev->smem_optin);
+  la.x_scale = x_scale;
+  la.w_scale = w_scale;
+  la.m = m;
+  la.n = n;
+  la.bias = static_cast<const __nv_bfloat16*>(bias);
+  la.y = static_cast<__nv_bfloat16*>(y);
+  la.wait_limit = kWaitLimitCycles;
+  la.status = dev->status;
+  cudaLaunchAttribute attrs[2];
+  cudaLaunchConfig_t cfg = pair_config(attrs, kI8Threads, linear_i8_smem(dev->smem_optin),
+                                       static_cast<long long>(la.tiles_m) * la.tiles_n, r > 0, dev, st);
+  note_launch();
+  if (cudaLaunchKernelEx(&cfg, linear_i8_pair_kernel, tmXq, tmWq, r > 0 ? tmP : tmXq, r > 0 ? tmB : tmWq, la) !=
+      cudaSuccess)
+    return DORA_ERR_CUDA;
+  return launch_error();
+}
+
+int dora_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const void* bias, const float* m,
+                           const float* n, float s, int64_t tokens, int64_t d_out, dora_dtype dt, void* y, int8_t* z8,
+                           float* z_scale, void* stream) {
+  if (dt != DORA_BF16 && dt != DORA_F32) return DORA_ERR_UNSUPPORTED;
+  if (tokens < 0 || d_out < 0) return DORA_ERR_INVALID_ARG;
+  if (tokens == 0 || d_out == 0) return DORA_OK;
+  if (!base_out || !lora_out || !m || !n || !y || !z8 || !z_scale) return DORA_ERR_INVALID_ARG;
+  if (tokens > INT32_MAX || d_out > INT32_MAX) return DORA_ERR_UNSUPPORTED;
+  const auto all_aligned = [&](size_t e) {
+    return aligned(base_out, e) && aligned(lora_out, e) && aligned(bias, e) && aligned(y, e);
+  };
+  if (dt == DORA_BF16 && (d_out % 8 != 0 || !all_aligned(16) || !aligned(z8, 8))) return DORA_ERR_UNSUPPORTED;
+  if (!all_aligned(4) || !aligned(m, 4) || !aligned(n, 4) || !aligned(z_scale, 4)) return DORA_ERR_UNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev)) return DORA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dt == DORA_BF16)
+    launch_compose_fwd_ckpt8<LanesBf16>(base_out, lora_out, bias, m, n, s, tokens, d_out, y, z8, z_scale, dev, st);
+  else if (d_out % 4 == 0 && all_aligned(16) && aligned(z8, 4))
+    launch_compose_fwd_ckpt8<LanesF32>(base_out, lora_out, bias, m, n, s, tokens, d_out, y, z8, z_scale, dev, st);
+  else
+    launch_compose_fwd_ckpt8<LanesF32Any>(base_out, lora_out, bias, m, n, s, tokens, d_out, y, z8, z_scale, dev, st);
+  return launch_error();
+}
+
+size_t dora_compose_bwd_ckpt8_workspace_size(int64_t tokens, int64_t d_out) {
+  if (tokens < 0 || d_out < 0) return 0;
+  const int64_t d = std::max<int64_t>(d_out, 1);
+  return align_up(static_cast<size_t>(cdiv(d, kCkptBlock)) * 8, 256) +
+         align_up(static_cast<size_t>(kMaxBwdChunks) * d * 4, 256);
+}
+
+int dora_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_scale, const float* m, const float* n,
+                           float s, int64_t tokens, int64_t d_out, dora_dtype dt, void* d_base, void* d_lora,
+                           float* d_m, void* workspace, size_t workspace_bytes, void* stream) {
+  if (dt != DORA_BF16 && dt != DORA_F32) return DORA_ERR_UNSUPPORTED;
+  if (tokens < 0 || d_out < 0) return DORA_ERR_INVALID_ARG;
+  if (d_out == 0) return DORA_OK;
+  if (!m || !n || !d_m) return DORA_ERR_INVALID_ARG;
+  if (tokens > 0 && (!dy || !z8 || !z_scale || !d_base || !d_lora)) return DORA_ERR_INVALID_ARG;
+  if (tokens > INT32_MAX || d_out > INT32_MAX) return DORA_ERR_UNSUPPORTED;
+  const auto all_aligned = [&](size_t e) { return aligned(dy, e) && aligned(d_base, e) && aligned(d_lora, e); };
+  if (dt == DORA_BF16 && (d_out % 8 != 0 || (tokens > 0 && (!all_aligned(16) || !aligned(z8, 8)))))
+    return DORA_ERR_UNSUPPORTED;
+  if (tokens > 0 && (!all_aligned(4) || !aligned(z_scale, 4))) return DORA_ERR_UNSUPPORTED;
+  if (!aligned(m, 4) || !aligned(n, 4) || !aligned(d_m, 4)) return DORA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < dora_compose_bwd_ckpt8_workspace_size(tokens, d_out)) return DORA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return DORA_ERR_UNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev)) return DORA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tokens == 0)
+    return cudaMemsetAsync(d_m, 0, static_cast<size_t>(d_out) * 4, st) == cudaSuccess ? DORA_OK : DORA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (dt == DORA_BF16)
+    launch_compose_bwd_ckpt8<LanesBf16>(dy, z8, z_scale, m, n, s, tokens, d_out, d_base, d_lora, d_m, ws, dev, st);
+  else if (d_out % 4 == 0 && all_aligned(16) && aligned(z8, 4))
+    launch_compose_bwd_ckpt8<LanesF32>(dy, z8, z_scale, m, n, s, tokens, d_out, d_base, d_lora, d_m, ws, dev, st);
+  else
+    launch_compose_bwd_ckpt8<LanesF32Any>(dy, z8, z_scale, m, n, s, tokens, d_out, d_base, d_lora, d_m, ws, dev, st);
+  return launch_error();
+}
 
 // ---------------------------------------------------- attached-norm backward
 namespace {

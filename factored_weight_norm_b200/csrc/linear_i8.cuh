@@ -1,0 +1,328 @@
+// linear_i8.cuh - the DoRA linear forward with the base weight and its input
+// in 8-bit integers, on tcgen05 tensor cores (sm_100a).
+//
+//   y = b + g * (sx_t * sw_o * sum_k xq[t,k] Wq[o,k] + sum_j P[t,j] B[o,j]),
+//   g = m / n,  P = bf16(s * x A^T)
+//
+// The base product runs in kind::i8 with int32 accumulation: exact, so its
+// order never shows.  The adapter's product runs in kind::f16 (bf16, fp32
+// accumulation) into an accumulator of its own, since the two differ in their
+// scales.  The epilogue joins them in fp32 with one rounding to bf16.
+#pragma once
+
+#include "linear_tc.cuh"
+
+namespace dora {
+
+constexpr int kI8Threads = 320;  // producer, MMA issuer, eight epilogue warps
+constexpr int kI8BK = 128;       // int8 K block: 128 bytes, as 64 bf16 are
+constexpr int64_t kI8MaxDIn = 131056;  // the largest multiple of 16 with 2^14 * d_in < 2^31
+constexpr int kI8EpiThreads = 256;
+// barriers: full / empty per stage, base and adapter accumulators full (one)
+// and empty (one each), drain; the TMEM slot and the abort flag
+constexpr size_t kI8BarrierBytes = 256;
+// per-column epilogue factors of two tiles: sw * g, g, b
+constexpr size_t kI8ColBytes = 2 * 3 * kPairBN * sizeof(float);
+
+struct LinearI8Args {
+  int M, N;              // tokens and output channels
+  int kb_main, kb_total; // K blocks of the int8 operands; total with the adapter's
+  int tiles_m, tiles_n;
+  int stages;
+  const float* x_scale;  // [M]
+  const float* w_scale;  // [N]
+  const float* m;        // [N], or null: g = 1
+  const float* n;
+  const __nv_bfloat16* bias;
+  __nv_bfloat16* y;      // [M, N]
+  long long wait_limit;
+  int* status;
+};
+
+__device__ __forceinline__ void lin_i8_tile(const LinearI8Args& a, int t, int& tm, int& tn) {
+  const int per_group = kLinGroupM * a.tiles_n;
+  const int g = t / per_group;
+  const int first = g * kLinGroupM;
+  const int gm = min(kLinGroupM, a.tiles_m - first);
+  const int rem = t - g * per_group;
+  tm = first + rem % gm;
+  tn = rem / gm;
+}
+
+// Synchronises the eight epilogue warps.
+__device__ __forceinline__ void epi_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kI8EpiThreads) : "memory");
+}
+
+// The pair GEMM of linear_tc.cuh (256 x 256 tiles, two K blocks per stage, the
+// same barriers and ring) with the int8 base in TMEM columns 0..255 and the
+// adapter in 256..511.  One tile's two accumulators fill the TMEM, so the next
+// tile's base product waits for the epilogue; to keep that wait short the
+// eight epilogue warps (two per lane quarter, 128 columns each) first pull
+// their whole base part into registers and release it, then finish the tile
+// beside the next main loop.  The next adapter product comes last in its tile,
+// long after its accumulator has been read.
+__global__ void __launch_bounds__(kI8Threads, 1)
+    linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                          const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmB,
+                          const LinearI8Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_s = smem_u32(smem_raw);
+  const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base_s - raw_s);
+  float* cols = reinterpret_cast<float*>(smem + a.stages * kPairStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(cols) + kI8ColBytes);
+  uint64_t* empty = full + a.stages;
+  uint64_t* acc_full = empty + a.stages;
+  uint64_t* base_empty = acc_full + 1;  // the even CTA's are used
+  uint64_t* ext_empty = base_empty + 1;
+  uint64_t* drain = ext_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cid = blockIdx.x >> 1;
+  const int n_pairs = gridDim.x >> 1;
+  const long long limit = a.wait_limit;
+  const int n_tiles = a.tiles_m * a.tiles_n;
+  const bool has_ext = a.kb_total > a.kb_main;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(base_empty, 16);  // eight epilogue warps in each CTA of the pair
+    mbar_init(ext_empty, 16);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmP);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 2 * kPairBN);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t parity_bits = 0;
+    uint32_t filled_mask = 0;
+    bool ext_ready = !has_ext;
+    bool ok = true;
+    for (int t = cid; t < n_tiles && ok; t += n_pairs) {
+      int tm, tn;
+      lin_i8_tile(a, t, tm, tn);
+      const int yx = tm * kPairBM + static_cast<int>(rank) * kLinBM;
+      const int yw = tn * kPairBN + static_cast<int>(rank) * (kPairBN / 2);
+      for (int kb0 = 0; kb0 < a.kb_total; kb0 += kPairKps) {
+        if (kb0 + kPairKps > a.kb_main && !ext_ready) {
+          grid_dep_wait();  // P comes from the launch before
+          fence_proxy_async_all();
+          ext_ready = true;
+        }
+        bool got = true;
+        if (lane == 0) {
+          got = mbar_wait(&empty[stage], phase ^ 1u, limit);
+          if (got && leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
+          if (!got) lin_timeout(a.status, abort_flag);
+        }
+        got = __shfl_sync(0xffffffffu, got, 0);
+        __syncwarp();
+        if (!got) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = base_s + stage * kPairStageBytes;
+        const uint32_t bar = full_leader + static_cast<uint32_t>(stage) * 8u;
+        if (lane < 2 * kPairKps) {
+          const bool w_side = lane >= kPairKps;
+          const int kb = kb0 + (w_side ? lane - kPairKps : lane);
+          // K blocks past kb_total lie wholly outside the tensor: zero-filled
+          const bool ext = has_ext && kb >= a.kb_main;
+          const int xk = ext ? (kb - a.kb_main) * kLinBK : kb * kI8BK;
+          const CUtensorMap* map = w_side ? (ext ? &tmB : &tmW) : (ext ? &tmP : &tmX);
+          tma_load_2d_pair(dst + lane * kLinABytes, map, bar, xk, w_side ? yw : yx);
+        }
+        parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+        filled_mask |= 1u << stage;
+        if (++stage == a.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // never leave a TMA copy in flight: the even CTA's full barriers count both CTAs' bytes
+    if (lane == 0 && leader)
+      for (int s2 = 0; s2 < a.stages; ++s2)
+        if ((filled_mask >> s2) & 1u) mbar_wait(&full[s2], (parity_bits >> s2) & 1u, limit);
+  } else if (warp == 1) {
+    // ------------------------------------------- MMA issuer (even CTA only)
+    if (leader && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const uint32_t idesc_b = idesc_i8_s32(kPairBM, kPairBN);
+      const uint32_t idesc_e = idesc_bf16_f32(kPairBM, kPairBN);
+      const uint64_t desc0 = sw128_kmajor_desc(base_s);
+      const uint64_t desc_step = kPairStageBytes >> 4;
+      uint32_t it = 0;
+      for (int t = cid; t < n_tiles && ok; t += n_pairs, ++it) {
+        if (!mbar_wait(base_empty, (it & 1u) ^ 1u, limit)) {
+          lin_timeout(a.status, abort_flag);
+          break;
+        }
+        tc_fence_after();
+        bool ext_free = false;
+        for (int kb0 = 0; kb0 < a.kb_total; kb0 += kPairKps) {
+          if (!mbar_wait(&full[stage], phase, limit)) {
+            lin_timeout(a.status, abort_flag);
+            ok = false;
+            break;
+          }
+          if (has_ext && !ext_free && kb0 + kPairKps > a.kb_main) {
+            if (!mbar_wait(ext_empty, (it & 1u) ^ 1u, limit)) {
+              lin_timeout(a.status, abort_flag);
+              ok = false;
+              break;
+            }
+            ext_free = true;
+          }
+          tc_fence_after();
+          const uint64_t adesc = desc0 + static_cast<uint64_t>(stage) * desc_step;
+          const uint64_t bdesc = adesc + ((kPairKps * kLinABytes) >> 4);
+#pragma unroll
+          for (int i = 0; i < kPairKps; ++i) {
+            const int kb = kb0 + i;
+            const uint64_t ad = adesc + i * (kLinABytes >> 4), bd = bdesc + i * (kLinABytes >> 4);
+            if (has_ext && kb >= a.kb_main) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_pair(tmem + kPairBN, ad + 2 * k, bd + 2 * k, idesc_e, (kb > a.kb_main || k > 0) ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_i8_pair(tmem, ad + 2 * k, bd + 2 * k, idesc_b, (kb > 0 || k > 0) ? 1u : 0u);
+            }
+          }
+          mma_commit_pair(&empty[stage], 0x3);
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) mma_commit_pair(acc_full, 0x3);
+      }
+      mma_commit_pair(drain, 0x1);
+      mbar_wait(drain, 0, limit);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    const int half = (warp - 2) >> 2;  // columns half * 128 .. of the tile
+    const int et = threadIdx.x - 64;
+    const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+    const uint32_t base_empty_leader = mapa_shared(smem_u32(base_empty), 0);
+    const uint32_t ext_empty_leader = mapa_shared(smem_u32(ext_empty), 0);
+    uint32_t it = 0;
+    bool alive = true;  // a warp whose wait gave up still meets the others at epi_sync
+    for (int t = cid; t < n_tiles; t += n_pairs, ++it) {
+      int tm, tn;
+      lin_i8_tile(a, t, tm, tn);
+      // this tile's column factors; the other half of the buffer may still be
+      // read by warps finishing the tile before
+      float* cf = cols + (it & 1u) * 3 * kPairBN;
+      {
+        const int c = tn * kPairBN + et;
+        float g = 0.f, sw = 0.f, b = 0.f;
+        if (c < a.N) {
+          g = a.m ? __ldg(a.m + c) / __ldg(a.n + c) : 1.f;
+          sw = __ldg(a.w_scale + c);
+          if (a.bias) b = __bfloat162float(a.bias[c]);
+        }
+        cf[et] = sw * g;
+        cf[kPairBN + et] = g;
+        cf[2 * kPairBN + et] = b;
+      }
+      const long long row = static_cast<long long>(tm) * kPairBM + rank * kLinBM + q * 32 + lane;
+      const bool row_ok = row < a.M;
+      const float sx = row_ok ? __ldg(a.x_scale + row) : 0.f;
+      epi_sync();
+      if (alive && !mbar_wait_warp(acc_full, it & 1u, limit)) {
+        if (lane == 0) lin_timeout(a.status, abort_flag);
+        alive = false;
+      }
+      if (!alive) continue;
+      tc_fence_after();
+      float v[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float u[32];
+        tmem_ld32(tmem_lane + c * 32, u);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[c * 32 + e] = static_cast<float>(__float_as_int(u[e])) * sx;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(base_empty_leader);
+      const int col0 = tn * kPairBN + half * 128;
+      const float* swg = cf + half * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float u[32];
+        if (has_ext) {
+          tmem_ld32(tmem_lane + kPairBN + c * 32, u);
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(ext_empty_leader);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (col0 + c * 32 + j * 8 >= a.N) continue;  // warp-uniform
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = c * 32 + j * 8 + e;
+            const float b = has_ext ? fmaf(swg[kPairBN + k], u[j * 8 + e], swg[2 * kPairBN + k]) : swg[2 * kPairBN + k];
+            o[e] = fmaf(v[k], swg[k], b);
+          }
+          if (row_ok) {
+            uint4 pk;
+            pk.x = pack_bf16x2(o[0], o[1]);
+            pk.y = pack_bf16x2(o[2], o[3]);
+            pk.z = pack_bf16x2(o[4], o[5]);
+            pk.w = pack_bf16x2(o[6], o[7]);
+            *reinterpret_cast<uint4*>(a.y + row * a.N + col0 + c * 32 + j * 8) = pk;
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 2 * kPairBN);
+}
+
+}  // namespace dora

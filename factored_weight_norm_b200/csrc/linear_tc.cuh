@@ -33,6 +33,7 @@
 // L2.  Every wait is bounded.
 #pragma once
 
+#include "quant8.cuh"
 #include "sm100_ptx.cuh"
 
 namespace dora {
@@ -62,6 +63,8 @@ struct LinearArgs {
   const __nv_bfloat16* bias;  // per-column bias, or null
   void* out;               // [M, ldo] row-major, bf16 or fp32 (kernel template)
   long long ldo;
+  int8_t* z8;              // CKPT: codes of the product itself, [M, ldo]
+  float* z_scale;          // CKPT: their scales, [M, ceil(N / 128)]
   int ext_waits;           // 1: the extension operands come from the preceding grid
   long long wait_limit;
   int* status;
@@ -104,7 +107,11 @@ constexpr uint32_t kPairStageBytes = 2 * kPairKps * kLinABytes;
 // B_MN: the B-side operand is stored N-contiguous (its rows run along K), as
 // W is for a contraction over d_out; it is loaded as two 64-column boxes per
 // K block and read through MN-major descriptors.  OUT_F32: fp32 output.
-template <bool B_MN, bool OUT_F32>
+// CKPT: the product z (before g and b) is kept too, as int8 codes with a scale
+// for every 128 columns (quant8.cuh); bn is then 128 or 256, so that a thread's
+// row of a tile holds whole stretches and their maximum needs no exchange.
+// The accumulator is read twice, once for the maxima and once for the codes.
+template <bool B_MN, bool OUT_F32, bool CKPT = false>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
                        const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2,
@@ -303,12 +310,39 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const long long row = static_cast<long long>(tm) * kPairBM + rank * kLinBM + q * 32 + lane;
       const bool row_ok = row < a.M;
       const float rscale = (row_ok && a.rs_num) ? __ldg(a.rs_num + row) / __ldg(a.rs_den + row) : 1.f;
+      uint32_t top = 0;
+      float inv = 0.f;
 #pragma unroll 1
       for (int c = 0; c < a.bn / 32; ++c) {
         const int col0 = tn * a.bn + c * 32;
         if (col0 >= a.N) break;  // warp-uniform
         float v[32];
+        if (CKPT && c % 4 == 0) {
+          // columns past N are zeros (zero-filled operands): they do not count
+          top = 0;
+#pragma unroll 1
+          for (int cc = c; cc < c + 4; ++cc) {
+            tmem_ld32(tmem_lane + static_cast<uint32_t>(ab * kPairBN + cc * 32), v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = max(top, abs_bits(v[e]));
+          }
+          inv = top_inverse(top);
+          if (row_ok) a.z_scale[row * ((a.N + 127) / 128) + col0 / 128] = top_scale(top);
+        }
         tmem_ld32(tmem_lane + static_cast<uint32_t>(ab * kPairBN + c * 32), v);
+        if (CKPT) {
+          int8_t* z_row = a.z8 + row * a.ldo;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float z[8];
+            uint32_t qc[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = v[8 * j + e];
+            codes_of<8>(z, top, inv, qc);
+            if (row_ok && col0 + 8 * j < a.N) CodeIO<8>::store(z_row + col0 + 8 * j, qc);
+          }
+          __syncwarp();
+        }
         const int my_col = col0 + lane;
         float gl = 0.f, bl = 0.f;
         if (my_col < a.N) {

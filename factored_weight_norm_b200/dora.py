@@ -99,7 +99,43 @@ SIGNATURES = {
         [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _f32, _i64, _i64, _i64, _i64,
          ctypes.c_int, _c_void_p, _c_void_p, _size, _c_void_p],
     ),
+    "dora_quantize_rows_i8": (
+        ctypes.c_int,
+        [_c_void_p, _c_void_p, _i64, _i64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
+    ),
+    "dora_rms_norm_i8": (
+        ctypes.c_int,
+        [_c_void_p, _c_void_p, _c_void_p, _f32, _i64, _i64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+         _c_void_p],
+    ),
+    "dora_dequantize_i8": (
+        ctypes.c_int,
+        [_c_void_p, _c_void_p, _i64, _i64, _i64, ctypes.c_int, _c_void_p, _c_void_p],
+    ),
+    "dora_linear_i8_fwd_workspace_size": (_size, [_i64, _i64]),
+    "dora_linear_i8_fwd": (
+        ctypes.c_int,
+        [_c_void_p] * 10 + [_f32, _i64, _i64, _i64, _i64, ctypes.c_int, _c_void_p, _c_void_p, _size, _c_void_p],
+    ),
+    "dora_compose_fwd_ckpt8": (
+        ctypes.c_int,
+        [_c_void_p] * 5 + [_f32, _i64, _i64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
+    ),
+    "dora_fused_linear_fwd_ckpt8": (
+        ctypes.c_int,
+        [_c_void_p] * 7 + [_f32, _i64, _i64, _i64, _i64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                           _size, _c_void_p],
+    ),
+    "dora_compose_bwd_ckpt8_workspace_size": (_size, [_i64, _i64]),
+    "dora_compose_bwd_ckpt8": (
+        ctypes.c_int,
+        [_c_void_p] * 5 + [_f32, _i64, _i64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size,
+                           _c_void_p],
+    ),
 }
+
+# columns of a row that share a scale in a checkpoint (the 8-bit format of include/dora.h)
+CKPT_BLOCK = 128
 
 _lib = None
 
@@ -414,13 +450,30 @@ def dora_fused_linear_fwd_workspace_size(tokens: int, r: int) -> int:
 
 def dora_fused_linear_fwd(x, W, A, B, m, n, s: float, bias=None, y=None, workspace=None, stream=None):
     """y = b + (m / n) * (x W^T + s * (x A^T) B^T), the compose fused into the GEMMs (bf16)."""
-    where = "dora_fused_linear_fwd"
+    return _fused_linear("dora_fused_linear_fwd", x, W, A, B, m, n, s, bias, y, None, None, workspace, stream)
+
+
+def dora_fused_linear_fwd_ckpt8(x, W, A, B, m, n, s: float, bias=None, y=None, z8=None, z_scale=None, workspace=None,
+                                stream=None):
+    """dora_fused_linear_fwd that keeps z = x W^T + s * (x A^T) B^T for the backward: (y, z8, z_scale).
+
+    z8 are int8 codes [tokens, d_out], z_scale their fp32 scales for every 128
+    columns of a token; ``dora_compose_bwd_ckpt8`` reads them."""
+    where = "dora_fused_linear_fwd_ckpt8"
+    if x.dim() != 2 or W.dim() != 2:
+        raise ValueError(f"{where}: x, W, A and B must be 2-D")
+    z8, z_scale = _checkpoint(where, x.shape[0], W.shape[0], z8, z_scale, x.device)
+    y = _fused_linear(where, x, W, A, B, m, n, s, bias, y, z8, z_scale, workspace, stream)
+    return y, z8, z_scale
+
+
+def _fused_linear(where, x, W, A, B, m, n, s, bias, y, z8, z_scale, workspace, stream):
     if x.dim() != 2 or W.dim() != 2 or A.dim() != 2 or B.dim() != 2:
         raise ValueError(f"{where}: x, W, A and B must be 2-D")
     T, d_in = x.shape
     d_out, r = W.shape[0], A.shape[0]
     if W.shape != (d_out, d_in) or A.shape != (r, d_in) or B.shape != (d_out, r):
-        raise ValueError("shape mismatch in dora_fused_linear_fwd")
+        raise ValueError(f"shape mismatch in {where}")
     _vec_f32(d_out, where, m=m, n=n)
     for t in (x, W, A, B):
         if t.dtype != torch.bfloat16:
@@ -429,17 +482,20 @@ def dora_fused_linear_fwd(x, W, A, B, m, n, s: float, bias=None, y=None, workspa
         raise ValueError("bias must be bf16 of shape (d_out,)")
     if y is not None and (tuple(y.shape) != (T, d_out) or y.dtype != torch.bfloat16):
         raise ValueError(f"{where}: y must be bf16 of shape ({T}, {d_out})")
-    _dense_cuda(x, W, A, B, m, n, bias, y, workspace)
+    _dense_cuda(x, W, A, B, m, n, bias, y, z8, z_scale, workspace)
     if y is None:
         y = torch.empty(T, d_out, dtype=torch.bfloat16, device=x.device)
     need = dora_fused_linear_fwd_workspace_size(T, r)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    st = lib().dora_fused_linear_fwd(
-        _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(bias), _ptr(m), _ptr(n), float(s), T, d_in, d_out, r, DORA_BF16,
-        _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream),
-    )
-    _check(st, "dora_fused_linear_fwd")
+    head = (_ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(bias), _ptr(m), _ptr(n), float(s), T, d_in, d_out, r, DORA_BF16,
+            _ptr(y))
+    tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    if z8 is None:
+        st = lib().dora_fused_linear_fwd(*head, *tail)
+    else:
+        st = lib().dora_fused_linear_fwd_ckpt8(*head, _ptr(z8), _ptr(z_scale), *tail)
+    _check(st, where)
     return y
 
 
@@ -477,3 +533,206 @@ def dora_factored_norm_bwd(W, A, B, s: float, n, d_n, dA=None, dB=None, workspac
     )
     _check(st, "dora_factored_norm_bwd")
     return dA, dB
+
+
+# ---------------------------------------------------------- 8-bit operators
+def _typed(where: str, name: str, t, shape, dtype):
+    """t (None skipped) has this shape and dtype."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
+
+
+def _checkpoint(where, tokens, d_out, z8, z_scale, device):
+    """(z8, z_scale) of a [tokens, d_out] checkpoint, checked or made."""
+    blocks = -(-d_out // CKPT_BLOCK)
+    _typed(where, "z8", z8, (tokens, d_out), torch.int8)
+    _typed(where, "z_scale", z_scale, (tokens, blocks), torch.float32)
+    if z8 is None:
+        z8 = torch.empty(tokens, d_out, dtype=torch.int8, device=device)
+    if z_scale is None:
+        z_scale = torch.empty(tokens, blocks, dtype=torch.float32, device=device)
+    return z8, z_scale
+
+
+def _rows_i8(where, x, residual, h, q, scale):
+    _acts2d(x, where)
+    rows, cols = x.shape
+    _like(x, where, residual=residual, h=h)
+    _typed(where, "q", q, (rows, cols), torch.int8)
+    _typed(where, "scale", scale, (rows,), torch.float32)
+    if h is not None and residual is None:
+        raise ValueError(f"{where}: h is x + residual, so it needs a residual")
+
+
+def _rows_i8_outputs(x, residual, h, q, scale):
+    rows, cols = x.shape
+    if residual is not None and h is None:
+        h = torch.empty_like(x)
+    if q is None:
+        q = torch.empty(rows, cols, dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    return h, q, scale
+
+
+def dora_quantize_rows_i8(x, residual=None, h=None, q=None, scale=None, stream=None):
+    """(q, scale, h): int8 codes and one fp32 scale for each row of h = x + residual.
+
+    h is written in x's type where there is a residual (it may be x or
+    residual itself) and None without one (the codes are x's)."""
+    where = "dora_quantize_rows_i8"
+    _rows_i8(where, x, residual, h, q, scale)
+    _dense_cuda(x, residual, h, q, scale)
+    h, q, scale = _rows_i8_outputs(x, residual, h, q, scale)
+    st = lib().dora_quantize_rows_i8(_ptr(x), _ptr(residual), x.shape[0], x.shape[1], _dt(x), _ptr(h), _ptr(q),
+                                     _ptr(scale), _stream(stream))
+    _check(st, where)
+    return q, scale, h
+
+
+def dora_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, want_y: bool = False, h=None, y=None, q=None,
+                     scale=None, stream=None):
+    """(q, scale, h, y): the root-mean-square norm of h = x + residual as int8 codes with one scale a row.
+
+    h as in dora_quantize_rows_i8; y is the norm in x's type (the adapter
+    branch's input), None unless it is passed or ``want_y`` is true."""
+    where = "dora_rms_norm_i8"
+    _rows_i8(where, x, residual, h, q, scale)
+    _like(x, where, y=y)
+    _typed(where, "weight", weight, (x.shape[1],), x.dtype)
+    _dense_cuda(x, weight, residual, h, y, q, scale)
+    h, q, scale = _rows_i8_outputs(x, residual, h, q, scale)
+    if y is None and want_y:
+        y = torch.empty_like(x)
+    st = lib().dora_rms_norm_i8(_ptr(x), _ptr(residual), _ptr(weight), float(eps), x.shape[0], x.shape[1], _dt(x),
+                                _ptr(h), _ptr(y), _ptr(q), _ptr(scale), _stream(stream))
+    _check(st, where)
+    return q, scale, h, y
+
+
+def dora_dequantize_i8(q, scale, dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """q * scale in ``dtype``; scale is [rows], or [rows, ceil(cols / 128)] as a checkpoint's."""
+    where = "dora_dequantize_i8"
+    if q.dim() != 2:
+        raise ValueError(f"{where}: q must be 2-D [rows, cols], got {tuple(q.shape)}")
+    rows, cols = q.shape
+    block = 0 if scale.dim() == 1 else CKPT_BLOCK
+    _typed(where, "q", q, (rows, cols), torch.int8)
+    _typed(where, "scale", scale, (rows,) if block == 0 else (rows, -(-cols // CKPT_BLOCK)), torch.float32)
+    dt = out.dtype if out is not None else dtype
+    _typed(where, "out", out, (rows, cols), dt)
+    if dt not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dt}: bf16 or fp32 only")
+    _dense_cuda(q, scale, out)
+    if out is None:
+        out = torch.empty(rows, cols, dtype=dt, device=q.device)
+    _check(lib().dora_dequantize_i8(_ptr(q), _ptr(scale), rows, cols, block, _dt(out), _ptr(out), _stream(stream)),
+           where)
+    return out
+
+
+def dora_linear_i8_fwd_workspace_size(tokens: int, r: int) -> int:
+    return int(lib().dora_linear_i8_fwd_workspace_size(tokens, r))
+
+
+def dora_linear_i8_fwd(x_q, x_scale, W_q, w_scale, x=None, A=None, B=None, m=None, n=None, s: float = 1.0, bias=None,
+                       y=None, workspace=None, stream=None):
+    """y = b + (m / n) * (x_scale w_scale (x_q W_q^T) + s * (x A^T) B^T) in bf16, from int8 rows and weights.
+
+    x, A and B (bf16) are the adapter's branch, all given or all None; m and n
+    both None is m / n = 1."""
+    where = "dora_linear_i8_fwd"
+    if x_q.dim() != 2 or W_q.dim() != 2:
+        raise ValueError(f"{where}: x_q and W_q must be 2-D")
+    T, d_in = x_q.shape
+    d_out = W_q.shape[0]
+    _typed(where, "x_q", x_q, (T, d_in), torch.int8)
+    _typed(where, "W_q", W_q, (d_out, d_in), torch.int8)
+    _typed(where, "x_scale", x_scale, (T,), torch.float32)
+    _typed(where, "w_scale", w_scale, (d_out,), torch.float32)
+    if len({x is None, A is None, B is None}) != 1:
+        raise ValueError(f"{where}: x, A and B come together")
+    if (m is None) != (n is None):
+        raise ValueError(f"{where}: m and n come together")
+    r = 0
+    if A is not None:
+        if A.dim() != 2:
+            raise ValueError(f"{where}: A must be 2-D")
+        r = A.shape[0]
+        _typed(where, "x", x, (T, d_in), torch.bfloat16)
+        _typed(where, "A", A, (r, d_in), torch.bfloat16)
+        _typed(where, "B", B, (d_out, r), torch.bfloat16)
+    _vec_f32(d_out, where, m=m, n=n)
+    _typed(where, "bias", bias, (d_out,), torch.bfloat16)
+    _typed(where, "y", y, (T, d_out), torch.bfloat16)
+    _dense_cuda(x_q, x_scale, W_q, w_scale, x, A, B, m, n, bias, y, workspace)
+    if y is None:
+        y = torch.empty(T, d_out, dtype=torch.bfloat16, device=x_q.device)
+    if workspace is None and r > 0:
+        workspace = torch.empty(dora_linear_i8_fwd_workspace_size(T, r), dtype=torch.uint8, device=x_q.device)
+    st = lib().dora_linear_i8_fwd(
+        _ptr(x_q), _ptr(x_scale), _ptr(W_q), _ptr(w_scale), _ptr(x), _ptr(A), _ptr(B), _ptr(bias), _ptr(m), _ptr(n),
+        float(s), T, d_in, d_out, r, DORA_BF16, _ptr(y), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream),
+    )
+    _check(st, where)
+    return y
+
+
+def dora_compose_fwd_ckpt8(base_out, lora_out, m, n, s: float, y=None, z8=None, z_scale=None, stream=None, bias=None):
+    """dora_compose_fwd that keeps z = (base_out - b) + s * lora_out for the backward: (y, z8, z_scale).
+
+    z8 are int8 codes [tokens, d_out], z_scale their fp32 scales for every 128
+    columns of a token; ``dora_compose_bwd_ckpt8`` reads them."""
+    where = "dora_compose_fwd_ckpt8"
+    _acts2d(base_out, where)
+    tokens, d_out = base_out.shape
+    _like(base_out, where, lora_out=lora_out, y=y)
+    _vec_f32(d_out, where, m=m, n=n)
+    _check_bias(bias, base_out, where)
+    z8, z_scale = _checkpoint(where, tokens, d_out, z8, z_scale, base_out.device)
+    _dense_cuda(base_out, lora_out, m, n, y, z8, z_scale, bias)
+    if y is None:
+        y = torch.empty_like(base_out)
+    st = lib().dora_compose_fwd_ckpt8(
+        _ptr(base_out), _ptr(lora_out), _ptr(bias), _ptr(m), _ptr(n), float(s), tokens, d_out, _dt(base_out), _ptr(y),
+        _ptr(z8), _ptr(z_scale), _stream(stream),
+    )
+    _check(st, where)
+    return y, z8, z_scale
+
+
+def dora_compose_bwd_ckpt8_workspace_size(tokens: int, d_out: int) -> int:
+    return int(lib().dora_compose_bwd_ckpt8_workspace_size(tokens, d_out))
+
+
+def dora_compose_bwd_ckpt8(dy, z8, z_scale, m, n, s: float, d_base=None, d_lora=None, d_m=None, workspace=None,
+                           stream=None):
+    """(d_base, d_lora, d_m) of the compose from its 8-bit checkpoint, with n held constant and the bias frozen."""
+    where = "dora_compose_bwd_ckpt8"
+    _acts2d(dy, where)
+    tokens, d_out = dy.shape
+    _like(dy, where, d_base=d_base, d_lora=d_lora)
+    _vec_f32(d_out, where, m=m, n=n, d_m=d_m)
+    _typed(where, "z8", z8, (tokens, d_out), torch.int8)
+    _typed(where, "z_scale", z_scale, (tokens, -(-d_out // CKPT_BLOCK)), torch.float32)
+    _dense_cuda(dy, z8, z_scale, m, n, d_base, d_lora, d_m, workspace)
+    if d_base is None:
+        d_base = torch.empty_like(dy)
+    if d_lora is None:
+        d_lora = torch.empty_like(dy)
+    if d_m is None:
+        d_m = torch.empty(d_out, dtype=torch.float32, device=dy.device)
+    if workspace is None:
+        workspace = torch.empty(dora_compose_bwd_ckpt8_workspace_size(tokens, d_out), dtype=torch.uint8,
+                                device=dy.device)
+    st = lib().dora_compose_bwd_ckpt8(
+        _ptr(dy), _ptr(z8), _ptr(z_scale), _ptr(m), _ptr(n), float(s), tokens, d_out, _dt(dy), _ptr(d_base),
+        _ptr(d_lora), _ptr(d_m), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream),
+    )
+    _check(st, where)
+    return d_base, d_lora, d_m

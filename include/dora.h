@@ -12,6 +12,8 @@
  * norm detached (with or without a base-layer bias, with or without a
  * workspace), the compose fused into the GEMMs that produce its inputs, and
  * the norm's own gradients into A and B for training with the norm attached.
+ * Beside them the 8-bit forms: an int8 linear with the norm and quantisers
+ * that make its input, and composes that keep their backward's input in 8 bits.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -308,6 +310,122 @@ DORA_API int dora_fused_linear_fwd(const void* x, const void* W, const void* A, 
                                    const float* m, const float* n, float s, int64_t tokens, int64_t d_in,
                                    int64_t d_out, int64_t r, dora_dtype dt, void* y, void* workspace,
                                    size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------ 8-bit operators
+ *
+ * One 8-bit format serves the integer product and the checkpoints.  A stretch
+ * of values v is kept as int8 codes q and one fp32 scale:
+ *
+ *   top = max |v|,  scale = top / 127,  q = 127 v / top rounded to the nearest
+ *   integer (ties to even, of the exact quotient);  the value kept is q * scale
+ *
+ * so each value is off by at most scale / 2.  A stretch is a whole row (a
+ * token's activations, an output channel's weights; scales [rows]) or, in a
+ * checkpoint, 128 columns of a row (scales [rows, ceil(cols / 128)], the last
+ * stretch shorter).  Codes are [rows, cols], row-major, in [-127, 127].  A
+ * stretch whose values are all below 2^-100 keeps zeros and the scale 0; one
+ * that holds an infinity or a NaN gets the scale NaN, so that all its values
+ * come back as NaN.  The pages have no 8-bit form; these calls have no
+ * counterpart there. */
+
+/* The 8-bit rows of x (+ residual) without a norm: the input of a projection
+ * that follows no norm, or a weight's output channels (quantised once).
+ * x: [rows, cols] in dt.  residual: [rows, cols] in dt or NULL; with one, h
+ * [rows, cols] = x + residual rounded to dt is written (h may be x or residual
+ * itself) and the codes are h's.  q: [rows, cols]; scale: fp32 [rows].  bf16:
+ * cols a multiple of 8, x, residual and h 16-byte aligned, q 8-byte aligned;
+ * fp32: any width, 4-byte aligned.  rows == 0 does nothing; cols == 0 is
+ * DORA_ERR_UNSUPPORTED. */
+DORA_API int dora_quantize_rows_i8(const void* x, const void* residual, int64_t rows, int64_t cols, dora_dtype dt,
+                                   void* h, int8_t* q, float* scale, void* stream);
+
+/* Root-mean-square norm with the residual's addition and an 8-bit output: the
+ * input of dora_linear_i8_fwd.  With h = x + residual as above (h = x without a
+ * residual, nothing written):
+ *
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  q, scale = 8-bit rows of h * weight * rstd
+ *   y = h * weight * rstd rounded to dt   (skipped when y is NULL)
+ *
+ * fp32 arithmetic; the codes come from h * weight alone (rstd is one factor of
+ * a row's values and enters its scale only).  weight: [d] in dt.  eps >= 0.  A
+ * row whose mean square leaves fp32's range gets the scale NaN.  Shapes,
+ * alignment and errors as dora_quantize_rows_i8. */
+DORA_API int dora_rms_norm_i8(const void* x, const void* residual, const void* weight, float eps, int64_t tokens,
+                              int64_t d, dora_dtype dt, void* h, void* y, int8_t* q, float* scale, void* stream);
+
+/* out[i, j] = q[i, j] * scale, rounded once to dt.  block = 0: scale is fp32
+ * [rows]; block = 128: fp32 [rows, ceil(cols / 128)] (a checkpoint's); other
+ * values are DORA_ERR_UNSUPPORTED.  Any width; q, out with their types'
+ * alignment (16-byte aligned out and widths of 8 columns run fastest). */
+DORA_API int dora_dequantize_i8(const int8_t* q, const float* scale, int64_t rows, int64_t cols, int64_t block,
+                                dora_dtype dt, void* out, void* stream);
+
+/* Bytes of workspace dora_linear_i8_fwd needs: the [tokens, r] bf16
+ * intermediate P = s * x A^T (at least 256; none is read when r == 0). */
+DORA_API size_t dora_linear_i8_fwd_workspace_size(int64_t tokens, int64_t r);
+
+/* The DoRA linear forward with the base weight and its input in 8 bits:
+ *
+ *   y = b + g * (x_scale[t] * w_scale[o] * sum_k x_q[t,k] W_q[o,k]
+ *                + s * ((x A^T) B^T)[t,o]),                 g = m / n
+ *
+ * an int8 tcgen05 product (int32 accumulation, exact) with a scale for each
+ * token and each output channel; the adapter's branch runs beside it in bf16
+ * (P = bf16(s * x A^T), fp32 accumulation) and both meet in the epilogue in
+ * fp32, with one rounding to bf16.
+ *
+ * x_q: int8 [tokens, d_in]; x_scale: fp32 [tokens]; W_q: int8 [d_out, d_in];
+ * w_scale: fp32 [d_out] (all codes from -128 on are allowed).  x: bf16
+ * [tokens, d_in], the rows the codes were made of, read by the adapter only; A:
+ * bf16 [r, d_in]; B: bf16 [d_out, r]; r == 0 is no adapter (x, A, B unread, no
+ * workspace).  bias: bf16 [d_out] or NULL.  m, n: fp32 [d_out], or both NULL for
+ * g = 1 (the plain 8-bit product); n is dora_factored_norm of the weight the
+ * codes stand for.  y: bf16 [tokens, d_out], not overlapping the inputs.  All
+ * row-major, codes, x, A, B and y 16-byte aligned; d_in a multiple of 16, at
+ * most 131056 (int32's range), d_out and r multiples of 8.  Only DORA_BF16.
+ * workspace as dora_fused_linear_fwd's, one call at a time.  Asynchronous on
+ * `stream`; tokens == 0 or d_out == 0 launches nothing. */
+DORA_API int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_q, const float* w_scale,
+                                const void* x, const void* A, const void* B, const void* bias, const float* m,
+                                const float* n, float s, int64_t tokens, int64_t d_in, int64_t d_out, int64_t r,
+                                dora_dtype dt, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* dora_compose_fwd_bias that also keeps what its backward needs of the two
+ * activations, z = (base - b) + s * lora (fp32, each operation rounded), in 8
+ * bits: 1.03 bytes an element instead of base_out and lora_out.  y is
+ * dora_compose_fwd_bias's, bit for bit (bias may be NULL).  z8: int8
+ * [tokens, d_out]; z_scale: fp32 [tokens, ceil(d_out / 128)].  bf16: d_out a
+ * multiple of 8, z8 8-byte aligned, the rest as there; fp32: any shape. */
+DORA_API int dora_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const void* bias, const float* m,
+                                    const float* n, float s, int64_t tokens, int64_t d_out, dora_dtype dt, void* y,
+                                    int8_t* z8, float* z_scale, void* stream);
+
+/* dora_fused_linear_fwd that also keeps z = x W^T + s (x A^T) B^T in 8 bits, as
+ * dora_compose_fwd_ckpt8 does (z in fp32 as it leaves the product, before g and
+ * b): the fused forward writes neither activation, so this is its training
+ * form.  y is dora_fused_linear_fwd's arithmetic.  z8 16-byte aligned; the
+ * rest, the workspace's size included, as there. */
+DORA_API int dora_fused_linear_fwd_ckpt8(const void* x, const void* W, const void* A, const void* B, const void* bias,
+                                         const float* m, const float* n, float s, int64_t tokens, int64_t d_in,
+                                         int64_t d_out, int64_t r, dora_dtype dt, void* y, int8_t* z8, float* z_scale,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace dora_compose_bwd_ckpt8 needs: partial sums of d_m, O(d_out). */
+DORA_API size_t dora_compose_bwd_ckpt8_workspace_size(int64_t tokens, int64_t d_out);
+
+/* dora_compose_bwd from a checkpoint (n constant, any bias already out of z):
+ *
+ *   d_base = g * dy,   d_lora = s * g * dy,   d_m_i = (sum_t dy[t,i] * z[t,i]) / n_i,
+ *   z = z8 * z_scale
+ *
+ * z8, z_scale from dora_compose_fwd_ckpt8 or dora_fused_linear_fwd_ckpt8.  A
+ * stretch with the scale NaN makes d_m NaN in its columns.  Types, alignment,
+ * the token reduction's order and the workspace's rules as dora_compose_bwd
+ * (z8 8-byte aligned for bf16); a workspace serves one call at a time. */
+DORA_API int dora_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_scale, const float* m,
+                                    const float* n, float s, int64_t tokens, int64_t d_out, dora_dtype dt,
+                                    void* d_base, void* d_lora, float* d_m, void* workspace, size_t workspace_bytes,
+                                    void* stream);
 
 /* Human-readable name of a dora_status value (static storage). */
 DORA_API const char* dora_status_string(int status);

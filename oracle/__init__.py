@@ -2,8 +2,8 @@
 
 Test infrastructure: only ``tests/``, ``__graft_entry__.smoke()`` and the CPU
 baseline legs of ``bench.py`` import it.  The product path never does.
-Every function is pinned by ``tests/test_oracle_pins.py``; no function is
-"parity unpinned".
+Every function is pinned by ``tests/test_oracle_pins.py`` (the 8-bit format's
+by ``tests/test_eight_bit.py``); no function is "parity unpinned".
 """
 
 from .dora_oracle import (  # noqa: F401
@@ -16,4 +16,11 @@ from .dora_oracle import (  # noqa: F401
     norm_backward,
     row_norm,
     row_norm_rows,
+)
+from .eight_bit import (  # noqa: F401
+    compose_backward_kept,
+    decode,
+    encode,
+    linear_i8,
+    rms_factor,
 )

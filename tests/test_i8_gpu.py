@@ -1,0 +1,361 @@
+"""The 8-bit rows (quantiser, norm, reader) and the int8 linear against fp64.
+
+Codes are integers defined by the rounding of an exact quotient, so they are
+compared for equality: with bf16 rows every value (and every product with a
+bf16 weight) is exact in fp32, with fp32 rows the product is rounded to fp32
+once on both sides.  Tolerances, with u = 2^-8 (half a bf16 step) and
+e = 2^-24 (half an fp32 step), both relative to the value:
+  * a plain row's scale is one fp32 division: equal to the rounded quotient;
+  * the norm's factor: a sum of d squares is off by at most d e of itself, so
+    its root by d e / 2, and four more operations round: (d / 2 + 4) e;
+  * a bf16 output adds u of its value;
+  * the linear: P is an fp32 sum of d_in terms rounded to bf16, the adapter's
+    product a sum of r more, the epilogue at most eight roundings.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from factored_weight_norm_b200 import dora as D
+from tests import parity as P
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U, E = 2.0 ** -8, 2.0 ** -24
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _gen(seed):
+    return torch.Generator(device="cpu").manual_seed(seed)
+
+
+def _rows(rows, cols, dtype, seed):
+    g = _gen(seed)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(0.5 * torch.randn(cols, generator=g))
+    return x.to(dtype).to(DEV)
+
+
+def _host(t):
+    return t.detach().cpu().numpy() if t.dtype != BF else P.f64(t)
+
+
+def _assert_within(got, ref, tol, what):
+    err = np.abs(P.f64(got) - ref)
+    assert np.all(err <= tol), f"{what}: {np.max(err - tol)} over its bound at {np.argwhere(err > tol)[0]}"
+
+
+# every thread layout: one, two and four vectors a thread, few and many rows,
+# scalar fp32 rows, and rows longer than the registers of one CTA
+ROWS = [(1, 8, BF), (3, 264, BF), (1, 8192, BF), (400, 2048, BF), (301, 4096, BF), (300, 8192, BF), (297, 16384, BF),
+        (2, 32768, BF), (2, 33000, BF), (1, 1, F32), (5, 33, F32), (2, 4099, F32), (300, 4099, F32), (300, 6000, F32),
+        (299, 1024, F32), (1, 8192, F32), (2, 33001, F32), (2, 40000, F32)]
+
+
+@pytest.mark.parametrize("rows, cols, dtype", ROWS, ids=lambda v: str(v).replace("torch.", ""))
+@pytest.mark.parametrize("residual", [False, True])
+def test_quantize_rows(rows, cols, dtype, residual):
+    x = _rows(rows, cols, dtype, 1)
+    res = _rows(rows, cols, dtype, 2) if residual else None
+    q, scale, h = D.dora_quantize_rows_i8(x, residual=res)
+    torch.cuda.synchronize()
+    want_h = x if res is None else (x.float() + res.float()).to(dtype)
+    assert (h is None) if res is None else torch.equal(h, want_h)
+    codes, sc = oracle.encode(P.f64(want_h))
+    assert np.array_equal(q.cpu().numpy(), codes)
+    assert np.array_equal(scale.cpu().numpy(), sc[:, 0].astype(np.float32))
+
+
+def _norm_reference(h, w, eps, dtype):
+    v = P.f64(h) * P.f64(w) if dtype == BF else (h.cpu().numpy() * w.cpu().numpy()).astype(np.float64)
+    codes, sc = oracle.encode(v)
+    f = oracle.rms_factor(P.f64(h), eps)
+    return codes, sc * f, v * f
+
+
+@pytest.mark.parametrize("rows, cols, dtype", ROWS, ids=lambda v: str(v).replace("torch.", ""))
+@pytest.mark.parametrize("residual", [False, True])
+def test_rms_norm(rows, cols, dtype, residual):
+    eps = 1e-5
+    x = _rows(rows, cols, dtype, 3)
+    res = _rows(rows, cols, dtype, 4) if residual else None
+    w = (1 + 0.2 * torch.randn(cols, generator=_gen(5))).to(dtype).to(DEV)
+    q, scale, h, y = D.dora_rms_norm_i8(x, w, eps, residual=res, want_y=True)
+    q2, scale2, _, y2 = D.dora_rms_norm_i8(x, w, eps, residual=res)
+    torch.cuda.synchronize()
+    want_h = x if res is None else (x.float() + res.float()).to(dtype)
+    assert (h is None) if res is None else torch.equal(h, want_h)
+    assert y2 is None and torch.equal(q, q2) and torch.equal(scale, scale2)
+    codes, sc, v = _norm_reference(want_h, w, eps, dtype)
+    assert np.array_equal(q.cpu().numpy(), codes)
+    rel = (cols / 2 + 5) * E
+    _assert_within(scale, sc[:, 0], rel * sc[:, 0], "scale")
+    _assert_within(y, v, (rel + E + (U if dtype == BF else 0)) * np.abs(v) * (1 + U), "y")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rms_norm_updates_the_residual_stream_in_place(dtype):
+    x, res = _rows(64, 1024, dtype, 6), _rows(64, 1024, dtype, 7)
+    w = torch.ones(1024, dtype=dtype, device=DEV)
+    q, scale, h, _ = D.dora_rms_norm_i8(x, w, residual=res)
+    for keep in ("residual", "x"):
+        a, b = x.clone(), res.clone()
+        out = b if keep == "residual" else a
+        q2, scale2, h2, _ = D.dora_rms_norm_i8(a, w, residual=b, h=out)
+        torch.cuda.synchronize()
+        assert h2 is out and torch.equal(out, h) and torch.equal(q2, q) and torch.equal(scale2, scale)
+    long_x, long_r = _rows(2, 40000, dtype, 8), _rows(2, 40000, dtype, 9)
+    q, scale, h = D.dora_quantize_rows_i8(long_x, residual=long_r)
+    q2, scale2, _ = D.dora_quantize_rows_i8(long_x, residual=long_r, h=long_r)
+    torch.cuda.synchronize()
+    assert torch.equal(long_r, h) and torch.equal(q2, q) and torch.equal(scale2, scale)
+
+
+@pytest.mark.parametrize("dtype, cols", [(BF, 512), (F32, 512), (F32, 513), (BF, 40000)])
+def test_rows_at_the_format_s_edges(dtype, cols):
+    x = torch.randn(12, cols, generator=_gen(10))
+    x[0] = 0.0
+    x[1, 3] = float("inf")
+    x[2, 5] = float("nan")
+    x[3] = 1e-31
+    x[4] = torch.finfo(dtype).max
+    x[5] = torch.arange(cols) % 255 / 254.0  # power-of-two tops: exact halves
+    x[6] = torch.where(torch.arange(cols) % 2 == 0, 1.0, 0.5)
+    x[7] = 2.0 ** -100
+    x[8] = -127.0
+    x[9, 1:] = 0.0
+    x[10] = 2.0 ** -126
+    x[11] = (torch.arange(cols) % 8 + 0.5) * (127.0 if dtype == F32 else 128.0) / 128.0
+    x = x.to(dtype).to(DEV)
+    q, scale, _ = D.dora_quantize_rows_i8(x)
+    v = D.dora_dequantize_i8(q, scale, dtype=F32)
+    torch.cuda.synchronize()
+    codes, sc = oracle.encode(P.f64(x))
+    assert np.array_equal(q.cpu().numpy(), codes)
+    assert np.array_equal(scale.cpu().numpy(), sc[:, 0].astype(np.float32), equal_nan=True)
+    assert torch.isnan(v[1]).all() and torch.isnan(v[2]).all() and not v[0].any() and not v[3].any()
+    # a norm whose squares leave fp32's range must not come back as numbers
+    q, scale, _, y = D.dora_rms_norm_i8(x, torch.ones(cols, dtype=dtype, device=DEV), want_y=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(scale[[1, 2, 4]]).all() and scale[0] == 0 and not y[0].any()
+    assert torch.isfinite(scale[[0, 3, 5, 6, 7, 8, 9, 10, 11]]).all()
+
+
+@pytest.mark.parametrize("rows, cols, block", [(1, 1, 0), (3, 130, 128), (70, 128, 128), (5, 4099, 128),
+                                                (333, 2056, 128), (9, 1000, 0), (1, 8192, 0), (0, 16, 0), (2, 0, 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_dequantize(rows, cols, block, dtype):
+    g = _gen(11)
+    q = torch.randint(-128, 128, (rows, cols), generator=g, dtype=torch.int8).to(DEV)
+    scale = torch.rand((rows,) if block == 0 else (rows, -(-cols // 128)), generator=g).to(DEV)
+    out = D.dora_dequantize_i8(q, scale, dtype=dtype)
+    into = torch.empty_like(out)
+    assert D.dora_dequantize_i8(q, scale, out=into) is into
+    torch.cuda.synchronize()
+    wide = scale[:, None].expand(rows, cols) if block == 0 else scale.repeat_interleave(128, dim=1)[:, :cols]
+    want = (q.float() * wide).to(dtype)
+    assert torch.equal(out, want) and torch.equal(into, want)
+
+
+# ------------------------------------------------------------------- linear
+def _module(T, d_in, d_out, r, s=0.5, bias=True, mag=True, seed=20, full=False):
+    g = _gen(seed)
+    rn = lambda *k: torch.randn(*k, generator=g)  # noqa: E731
+    W = (0.02 * rn(d_out, d_in)).to(BF).to(DEV)
+    x = rn(T, d_in).to(BF).to(DEV)
+    if full:
+        xq = torch.randint(-128, 128, (T, d_in), generator=g, dtype=torch.int8).to(DEV)
+        wq = torch.randint(-128, 128, (d_out, d_in), generator=g, dtype=torch.int8).to(DEV)
+        xs, ws = torch.rand(T, generator=g).to(DEV), torch.rand(d_out, generator=g).to(DEV)
+    else:
+        xq, xs, _ = D.dora_quantize_rows_i8(x)
+        wq, ws, _ = D.dora_quantize_rows_i8(W)
+    k = dict(x_q=xq, x_scale=xs, W_q=wq, w_scale=ws, s=s)
+    if r:
+        k.update(x=x, A=((2 * torch.rand(r, d_in, generator=g) - 1) / d_in ** 0.5).to(BF).to(DEV),
+                 B=(0.02 * rn(d_out, r)).to(BF).to(DEV))
+    if mag:
+        k.update(m=(1 + 0.1 * rn(d_out)).to(DEV), n=(1 + 0.1 * torch.rand(d_out, generator=g)).to(DEV))
+    if bias:
+        k.update(bias=(0.3 * rn(d_out)).to(BF).to(DEV))
+    return k
+
+
+def _check_linear(k, y, rows=slice(None), cols=slice(None)):
+    f = lambda n, i=slice(None): None if k.get(n) is None else P.f64(k[n])[i]  # noqa: E731
+    ref = oracle.linear_i8(f("x_q", rows), f("x_scale", rows), f("W_q", cols), f("w_scale", cols), f("x", rows),
+                           f("A"), f("B", cols), f("m", cols), f("n", cols), k["s"], f("bias", cols))
+    g = np.abs(f("m", cols) / f("n", cols)) if k.get("m") is not None else np.ones(ref.shape[1])
+    base = np.abs(f("x_q", rows) @ f("W_q", cols).T) * np.outer(f("x_scale", rows), f("w_scale", cols))
+    low = low_err = 0.0
+    if k.get("A") is not None:
+        s, x, A, B = abs(k["s"]), np.abs(f("x", rows)), np.abs(f("A")), np.abs(f("B", cols))
+        Pm = s * np.abs(f("x", rows) @ f("A").T)          # |P|
+        p_err = x.shape[1] * E * s * (x @ A.T) + U * Pm   # its fp32 sum, then bf16
+        low = Pm @ B.T
+        low_err = p_err @ B.T * (1 + U) + A.shape[0] * E * low
+    b = 0.0 if k.get("bias") is None else np.abs(f("bias", cols))[None, :]
+    tol = g * (low_err + 8 * E * (base + low)) + 8 * E * b
+    _assert_within(np.asarray(P.f64(y))[rows][:, cols], ref, tol + U * (np.abs(ref) + tol), "y")
+
+
+LINEAR = [(1, 16, 8, 8), (1, 8192, 264, 384), (2, 144, 136, 0), (7, 1040, 1000, 48), (16, 528, 520, 64),
+          (17, 4112, 256, 16), (33, 2048, 4096, 384), (64, 272, 392, 72), (65, 512, 128, 8), (128, 1024, 2056, 0),
+          (129, 400, 264, 40), (200, 2064, 1000, 128), (256, 256, 2048, 64), (300, 640, 512, 384), (513, 1024, 776, 8),
+          (1030, 528, 264, 24)]
+
+
+@pytest.mark.parametrize("T, d_in, d_out, r", LINEAR)
+@pytest.mark.parametrize("bias, mag", [(True, True), (False, False)])
+def test_linear_i8(T, d_in, d_out, r, bias, mag):
+    k = _module(T, d_in, d_out, r, bias=bias, mag=mag)
+    y = D.dora_linear_i8_fwd(**k)
+    y2 = D.dora_linear_i8_fwd(**k)
+    torch.cuda.synchronize()
+    assert D.dora_device_status() == D.DORA_OK
+    assert torch.equal(y, y2)
+    _check_linear(k, y)
+
+
+@pytest.mark.parametrize("T, d_in, d_out, r", [(1, 528, 264, 8), (19, 2064, 136, 0), (140, 4096, 264, 16), (520, 656, 520, 8)])
+@pytest.mark.parametrize("s", [-1.75, 0.0])
+def test_linear_i8_all_codes_and_scales(T, d_in, d_out, r, s):
+    # every code from -128 to 127, negative and zero s
+    k = _module(T, d_in, d_out, r, s=s, full=True)
+    y = D.dora_linear_i8_fwd(**k)
+    torch.cuda.synchronize()
+    _check_linear(k, y)
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_linear_i8_reaches_the_end_of_int32(T):
+    # 131056 products of two lowest codes: 2^14 * 131056 = 2^31 - 2^18
+    d_in = 131056
+    k = dict(x_q=torch.full((T, d_in), -128, dtype=torch.int8, device=DEV), x_scale=torch.ones(T, device=DEV),
+             W_q=torch.full((8, d_in), -128, dtype=torch.int8, device=DEV), w_scale=torch.ones(8, device=DEV))
+    k["W_q"][1] = 127
+    y = D.dora_linear_i8_fwd(**k)
+    torch.cuda.synchronize()
+    want = torch.full((T, 8), float(2 ** 14 * d_in), device=DEV)
+    want[:, 1] = float(-128 * 127 * d_in)
+    assert torch.equal(y, want.to(BF))
+
+
+def test_linear_i8_zero_scales_and_nan_rows():
+    k = _module(5, 256, 264, 16, bias=True)
+    k["x_scale"] = k["x_scale"].clone()
+    k["x_scale"][1] = 0.0
+    k["x_scale"][3] = float("nan")
+    y = D.dora_linear_i8_fwd(**k)
+    torch.cuda.synchronize()
+    assert torch.isnan(y[3]).all() and torch.isfinite(y[[0, 1, 2, 4]]).all()
+
+
+def test_linear_i8_no_tokens_no_channels_and_a_rank_of_zero():
+    k = _module(0, 64, 256, 0)
+    assert D.dora_linear_i8_fwd(**k).shape == (0, 256)
+    k = _module(3, 64, 8, 0, bias=False, mag=False)
+    k.update(W_q=k["W_q"][:0].contiguous(), w_scale=k["w_scale"][:0].contiguous())
+    assert D.dora_linear_i8_fwd(**k).shape == (3, 0)
+    k = _module(3, 64, 16, 0)
+    y = D.dora_linear_i8_fwd(**k)
+    empty = dict(x=torch.zeros(3, 64, dtype=BF, device=DEV), A=torch.zeros(0, 64, dtype=BF, device=DEV),
+                 B=torch.zeros(16, 0, dtype=BF, device=DEV))
+    assert torch.equal(D.dora_linear_i8_fwd(**{**k, **empty}), y)
+
+
+@pytest.mark.parametrize("T", [1, 33, 300])
+def test_linear_i8_writes_only_its_rows_and_allocates_nothing(T):
+    k = _module(T, 512, 520, 64)
+    d_out = 520
+    buf = torch.full((T + 2, d_out), 7.0, dtype=BF, device=DEV)
+    y = buf[1:1 + T]
+    ws = torch.empty(D.dora_linear_i8_fwd_workspace_size(T, 64) + 256, dtype=torch.uint8, device=DEV).fill_(123)
+    work = ws[: D.dora_linear_i8_fwd_workspace_size(T, 64)]
+    ref = D.dora_linear_i8_fwd(**k)
+    torch.cuda.synchronize()
+    free0, _ = torch.cuda.mem_get_info()
+    D.dora_linear_i8_fwd(**k, y=y, workspace=work)
+    torch.cuda.synchronize()
+    assert torch.cuda.mem_get_info()[0] == free0
+    assert torch.equal(y, ref) and (buf[0] == 7).all() and (buf[-1] == 7).all()
+    assert (ws[work.numel():] == 123).all()
+    with pytest.raises(RuntimeError):
+        D.dora_linear_i8_fwd(**k, workspace=work[:16])
+
+
+def test_serving_chain_captured_and_replayed():
+    # norm -> gate-like projection -> quantised rows -> projection back, as a layer runs it
+    T, d, f, r = 3, 512, 1048, 32
+    up, down = _module(T, d, f, r, seed=31), _module(T, 1056, d, r, seed=32)
+    h0 = _rows(T, d, BF, 33)
+    stream = h0.clone()
+    x = _rows(T, d, BF, 34)
+    w = (1 + 0.1 * torch.randn(d, generator=_gen(35))).to(BF).to(DEV)
+    pad = torch.zeros(T, 1056, dtype=BF, device=DEV)
+    out = torch.empty(T, d, dtype=BF, device=DEV)
+    bufs = dict(q=torch.empty(T, d, dtype=torch.int8, device=DEV), scale=torch.empty(T, device=DEV),
+                y=torch.empty(T, d, dtype=BF, device=DEV))
+    mid = torch.empty(T, f, dtype=BF, device=DEV)
+    q2, s2 = torch.empty(T, 1056, dtype=torch.int8, device=DEV), torch.empty(T, device=DEV)
+    ws1 = torch.empty(D.dora_linear_i8_fwd_workspace_size(T, r), dtype=torch.uint8, device=DEV)
+    ws2 = torch.empty_like(ws1)
+
+    def layer():
+        D.dora_rms_norm_i8(x, w, residual=stream, h=stream, **bufs)
+        D.dora_linear_i8_fwd(**{**up, "x_q": bufs["q"], "x_scale": bufs["scale"], "x": bufs["y"]}, y=mid, workspace=ws1)
+        pad[:, :f].copy_(mid)
+        D.dora_quantize_rows_i8(pad, q=q2, scale=s2)
+        D.dora_linear_i8_fwd(**{**down, "x_q": q2, "x_scale": s2, "x": pad}, y=out, workspace=ws2)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer()
+    for seed in (36, 37):
+        stream.copy_(_rows(T, d, BF, seed))
+        x.copy_(_rows(T, d, BF, seed + 10))
+        keep = stream.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (stream, mid, out)]
+        stream.copy_(keep)
+        layer()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (stream, mid, out)):
+            assert torch.equal(a, b)
+        _check_linear({**up, "x_q": bufs["q"], "x_scale": bufs["scale"], "x": bufs["y"]}, mid)
+        _check_linear({**down, "x_q": q2, "x_scale": s2, "x": pad}, out)
+        codes, sc, _ = _norm_reference((x.float() + keep.float()).to(BF), w, 1e-6, BF)
+        assert np.array_equal(bufs["q"].cpu().numpy(), codes)
+    assert D.dora_device_status() == D.DORA_OK
+
+
+def test_two_streams_at_once():
+    a, b = _module(4, 2048, 1024, 64, seed=41), _module(300, 1024, 776, 16, seed=42)
+    ra, rb = D.dora_linear_i8_fwd(**a), D.dora_linear_i8_fwd(**b)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for _ in range(4):
+        for st, k, ref in zip(streams, (a, b), (ra, rb)):
+            with torch.cuda.stream(st):
+                outs.append((D.dora_linear_i8_fwd(**k), ref))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref) for y, ref in outs)
+    assert D.dora_device_status() == D.DORA_OK
+
+
+def test_linear_i8_headline_sampled():
+    # 8192 tokens through the 8192 x 8192 module at rank 384
+    k = _module(8192, 8192, 8192, 384, seed=51)
+    y = D.dora_linear_i8_fwd(**k)
+    torch.cuda.synchronize()
+    assert D.dora_device_status() == D.DORA_OK
+    _check_linear(k, y, rows=np.array([0, 127, 128, 255, 256, 4099, 8191]), cols=np.array([0, 127, 128, 300, 8191]))
