@@ -26,6 +26,7 @@ from .dora import (  # noqa: F401
     dora_factored_norm_workspace_size,
     dora_fused_linear_fwd,
     dora_fused_linear_fwd_ckpt8,
+    dora_fused_linear_fwd_ckpt8_workspace_size,
     dora_fused_linear_fwd_workspace_size,
     dora_launch_count,
     dora_linear_i8_fwd,

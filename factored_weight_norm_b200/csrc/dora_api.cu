@@ -20,6 +20,7 @@
 #include "../../include/dora.h"
 #include "ckpt8.cuh"
 #include "compose.cuh"
+#include "linear_ckpt8.cuh"
 #include "linear_i8.cuh"
 #include "linear_tc.cuh"
 #include "norm_bwd.cuh"
@@ -158,7 +159,7 @@ int device_info(DeviceInfo** out) {
         pair_attrs(linear_pair_kernel<false, true>, d.smem_optin) ||
         pair_attrs(linear_pair_kernel<true, true>, d.smem_optin) ||
         pair_attrs(linear_pair_kernel<false, false, true>, d.smem_optin) ||
-        pair_attrs(linear_i8_pair_kernel, d.smem_optin))
+        pair_attrs(linear_i8_pair_kernel, d.smem_optin) || pair_attrs(linear_ckpt8_pair_kernel, d.smem_optin))
       return DORA_ERR_CUDA;
     {
       cudaLaunchConfig_t occ{};
@@ -897,10 +898,11 @@ cudaLaunchConfig_t pair_config(cudaLaunchAttribute (&attrs)[2], int threads, siz
   return cfg;
 }
 
-// P = bf16(s * x A^T) into `P` [tokens, r]; ordered after everything before it
-// on the stream.  tmA has boxes of pick_bn(r) / 2 rows.
-int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, float s, int64_t tokens, int64_t d_in,
-             int64_t r, const DeviceInfo* dev, cudaStream_t st) {
+// P = bf16(s * x A^T) into `P` [tokens, r], what the rounding leaves into `P_lo`
+// unless that is null; ordered after everything before it on the stream.  tmA
+// has boxes of pick_bn(r) / 2 rows.
+int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, __nv_bfloat16* P_lo, float s,
+             int64_t tokens, int64_t d_in, int64_t r, const DeviceInfo* dev, cudaStream_t st) {
   LinearArgs pa{};
   pa.M = static_cast<int>(tokens);
   pa.N = static_cast<int>(r);
@@ -911,6 +913,7 @@ int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, f
   pa.stages = linear_pair_stages(dev->smem_optin);
   pa.alpha = s;
   pa.out = P;
+  pa.out_lo = P_lo;
   pa.ldo = r;
   pa.wait_limit = kWaitLimitCycles;
   pa.status = dev->status;
@@ -918,13 +921,11 @@ int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, f
   cudaLaunchConfig_t cfg = pair_config(attrs, kLinThreads, linear_pair_smem(dev->smem_optin),
                                        static_cast<long long>(pa.tiles_m) * pa.tiles_n, false, dev, st);
   note_launch();
-  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<false, false>, tmX, tmA, tmX, tmA, pa) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, P_lo ? linear_pair_kernel<false, false, true> : linear_pair_kernel<false, false>, tmX,
+                            tmA, tmX, tmA, pa) == cudaSuccess
              ? DORA_OK
              : DORA_ERR_CUDA;
 }
-
-// Tile width of a linear that keeps codes: a tile holds whole 128-column stretches.
-int pick_bn_ckpt(long long N) { return N <= kCkptBlock ? kCkptBlock : 256; }
 
 int fused_linear(const void* x, const void* W, const void* A, const void* B, const void* bias, const float* m,
                  const float* n, float s, int64_t tokens, int64_t d_in, int64_t d_out, int64_t r, dora_dtype dt,
@@ -943,8 +944,8 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
       !aligned(bias, 2) || !aligned(m, 4) || !aligned(n, 4) || !aligned(z8, 16) || !aligned(z_scale, 4))
     return DORA_ERR_UNSUPPORTED;
   if (cdiv(tokens, kPairBM) * cdiv(d_out, 128) > INT32_MAX) return DORA_ERR_UNSUPPORTED;
-  const size_t need = dora_fused_linear_fwd_workspace_size(tokens, r);
-  if (r > 0 && (!workspace || workspace_bytes < need)) return DORA_ERR_WORKSPACE;
+  const size_t p_bytes = dora_fused_linear_fwd_workspace_size(tokens, r);
+  if (r > 0 && (!workspace || workspace_bytes < (ckpt ? 2 : 1) * p_bytes)) return DORA_ERR_WORKSPACE;
   if (r > 0 && !aligned(workspace, 256)) return DORA_ERR_UNSUPPORTED;
   DeviceInfo* dev = nullptr;
   if (device_info(&dev)) return DORA_ERR_CUDA;
@@ -952,7 +953,7 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
   __nv_bfloat16* P = static_cast<__nv_bfloat16*>(workspace);
 
   // B-side boxes hold the bn / 2 rows one CTA of a pair owns
-  const int bn_p = r > 0 ? pick_bn(r) : 256, bn_y = ckpt ? pick_bn_ckpt(d_out) : pick_bn(d_out);
+  const int bn_p = r > 0 ? pick_bn(r) : 256, bn_y = ckpt ? kPairBN : pick_bn(d_out);
   CUtensorMap tmX, tmW, tmA, tmP, tmB;
   if (make_map(&tmX, x, tokens, d_in) || make_map(&tmW, W, d_out, d_in, bn_y / 2)) return DORA_ERR_CUDA;
   if (r > 0 && (make_map(&tmA, A, r, d_in, bn_p / 2) || make_map(&tmP, P, tokens, r) ||
@@ -962,7 +963,36 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
   const int stages = linear_pair_stages(dev->smem_optin);
   if (stages < 2) return DORA_ERR_UNSUPPORTED;
   const long long tiles_m2 = cdiv(tokens, kPairBM);
-  if (r > 0 && launch_p(tmX, tmA, P, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
+  __nv_bfloat16* P_lo = ckpt && r > 0 ? P + p_bytes / 2 : nullptr;
+  if (r > 0 && launch_p(tmX, tmA, P, P_lo, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
+  cudaLaunchAttribute attrs[2];
+  if (ckpt) {
+    CUtensorMap tmLo;
+    if (r > 0 && make_map(&tmLo, P_lo, tokens, r)) return DORA_ERR_CUDA;
+    LinearCkptArgs ca{};
+    ca.M = static_cast<int>(tokens);
+    ca.N = static_cast<int>(d_out);
+    ca.kb_main = kb_main;
+    ca.kb_r = static_cast<int>(cdiv(r, kLinBK));
+    ca.tiles_m = static_cast<int>(tiles_m2);
+    ca.tiles_n = static_cast<int>(cdiv(d_out, kPairBN));
+    ca.stages = linear_i8_stages(dev->smem_optin);
+    ca.m = m;
+    ca.n = n;
+    ca.bias = static_cast<const __nv_bfloat16*>(bias);
+    ca.y = static_cast<__nv_bfloat16*>(y);
+    ca.z8 = z8;
+    ca.z_scale = z_scale;
+    ca.wait_limit = kWaitLimitCycles;
+    ca.status = dev->status;
+    cudaLaunchConfig_t cfg = pair_config(attrs, kI8Threads, linear_i8_smem(dev->smem_optin),
+                                         static_cast<long long>(ca.tiles_m) * ca.tiles_n, r > 0, dev, st);
+    note_launch();
+    if (cudaLaunchKernelEx(&cfg, linear_ckpt8_pair_kernel, tmX, tmW, r > 0 ? tmP : tmX, r > 0 ? tmLo : tmX,
+                           r > 0 ? tmB : tmW, ca) != cudaSuccess)
+      return DORA_ERR_CUDA;
+    return launch_error();
+  }
 
   // 2) y = bf16(g * [x | P] [W | B]^T + b), dependent on 1) only for the extension blocks
   LinearArgs la{};
@@ -980,19 +1010,15 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
   la.bias = static_cast<const __nv_bfloat16*>(bias);
   la.out = static_cast<__nv_bfloat16*>(y);
   la.ldo = d_out;
-  la.z8 = z8;
-  la.z_scale = z_scale;
   la.ext_waits = r > 0 ? 1 : 0;
   la.wait_limit = kWaitLimitCycles;
   la.status = dev->status;
-  cudaLaunchAttribute attrs[2];
   cudaLaunchConfig_t cfg = pair_config(attrs, kLinThreads, linear_pair_smem(dev->smem_optin),
                                        static_cast<long long>(la.tiles_m) * la.tiles_n, r > 0, dev, st);
   const CUtensorMap& tmA2 = r > 0 ? tmP : tmX;
   const CUtensorMap& tmB2 = r > 0 ? tmB : tmW;
   note_launch();
-  if (cudaLaunchKernelEx(&cfg, ckpt ? linear_pair_kernel<false, false, true> : linear_pair_kernel<false, false>, tmX,
-                         tmW, tmA2, tmB2, la) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<false, false>, tmX, tmW, tmA2, tmB2, la) != cudaSuccess)
     return DORA_ERR_CUDA;
   return launch_error();
 }
@@ -1007,6 +1033,10 @@ int dora_fused_linear_fwd(const void* x, const void* W, const void* A, const voi
                           dora_dtype dt, void* y, void* workspace, size_t workspace_bytes, void* stream) {
   return fused_linear(x, W, A, B, bias, m, n, s, tokens, d_in, d_out, r, dt, y, false, nullptr, nullptr, workspace,
                       workspace_bytes, stream);
+}
+
+size_t dora_fused_linear_fwd_ckpt8_workspace_size(int64_t tokens, int64_t r) {
+  return 2 * dora_fused_linear_fwd_workspace_size(tokens, r);
 }
 
 int dora_fused_linear_fwd_ckpt8(const void* x, const void* W, const void* A, const void* B, const void* bias,
@@ -1203,7 +1233,7 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
     if (make_map(&tmX, x, tokens, d_in) || make_map(&tmA, A, r, d_in, pick_bn(r) / 2) || make_map(&tmP, P, tokens, r) ||
         make_map(&tmB, B, d_out, r, kPairBN / 2))
       return DORA_ERR_CUDA;
-    if (launch_p(tmX, tmA, P, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
+    if (launch_p(tmX, tmA, P, nullptr, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
   }
   LinearI8Args la{};
   la.M = static_cast<int>(tokens);

@@ -39,18 +39,9 @@ struct LinearI8Args {
   int* status;
 };
 
-__device__ __forceinline__ void lin_i8_tile(const LinearI8Args& a, int t, int& tm, int& tn) {
-  const int per_group = kLinGroupM * a.tiles_n;
-  const int g = t / per_group;
-  const int first = g * kLinGroupM;
-  const int gm = min(kLinGroupM, a.tiles_m - first);
-  const int rem = t - g * per_group;
-  tm = first + rem % gm;
-  tn = rem / gm;
-}
-
 // Synchronises the eight epilogue warps.
 __device__ __forceinline__ void epi_sync() {
+  __syncwarp();
   asm volatile("bar.sync 1, %0;" ::"n"(kI8EpiThreads) : "memory");
 }
 
@@ -129,7 +120,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     bool ok = true;
     for (int t = cid; t < n_tiles && ok; t += n_pairs) {
       int tm, tn;
-      lin_i8_tile(a, t, tm, tn);
+      lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
       const int yx = tm * kPairBM + static_cast<int>(rank) * kLinBM;
       const int yw = tn * kPairBN + static_cast<int>(rank) * (kPairBN / 2);
       for (int kb0 = 0; kb0 < a.kb_total; kb0 += kPairKps) {
@@ -245,7 +236,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     bool alive = true;  // a warp whose wait gave up still meets the others at epi_sync
     for (int t = cid; t < n_tiles; t += n_pairs, ++it) {
       int tm, tn;
-      lin_i8_tile(a, t, tm, tn);
+      lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
       // this tile's column factors; the other half of the buffer may still be
       // read by warps finishing the tile before
       float* cf = cols + (it & 1u) * 3 * kPairBN;

@@ -33,7 +33,6 @@
 // L2.  Every wait is bounded.
 #pragma once
 
-#include "quant8.cuh"
 #include "sm100_ptx.cuh"
 
 namespace dora {
@@ -63,18 +62,18 @@ struct LinearArgs {
   const __nv_bfloat16* bias;  // per-column bias, or null
   void* out;               // [M, ldo] row-major, bf16 or fp32 (kernel template)
   long long ldo;
-  int8_t* z8;              // CKPT: codes of the product itself, [M, ldo]
-  float* z_scale;          // CKPT: their scales, [M, ceil(N / 128)]
+  __nv_bfloat16* out_lo;   // SPLIT: the rest of a bf16 output, [M, ldo]
   int ext_waits;           // 1: the extension operands come from the preceding grid
   long long wait_limit;
   int* status;
 };
 
-__device__ __forceinline__ void lin_tile(const LinearArgs& a, int t, int& tm, int& tn) {
-  const int per_group = kLinGroupM * a.tiles_n;
+// Tile t of the walk: groups of kLinGroupM tiles along M, along N within a group.
+__device__ __forceinline__ void lin_tile_of(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int per_group = kLinGroupM * tiles_n;
   const int g = t / per_group;
   const int first = g * kLinGroupM;
-  const int gm = min(kLinGroupM, a.tiles_m - first);
+  const int gm = min(kLinGroupM, tiles_m - first);
   const int rem = t - g * per_group;
   tm = first + rem % gm;
   tn = rem / gm;
@@ -107,11 +106,9 @@ constexpr uint32_t kPairStageBytes = 2 * kPairKps * kLinABytes;
 // B_MN: the B-side operand is stored N-contiguous (its rows run along K), as
 // W is for a contraction over d_out; it is loaded as two 64-column boxes per
 // K block and read through MN-major descriptors.  OUT_F32: fp32 output.
-// CKPT: the product z (before g and b) is kept too, as int8 codes with a scale
-// for every 128 columns (quant8.cuh); bn is then 128 or 256, so that a thread's
-// row of a tile holds whole stretches and their maximum needs no exchange.
-// The accumulator is read twice, once for the maxima and once for the codes.
-template <bool B_MN, bool OUT_F32, bool CKPT = false>
+// SPLIT: what the bf16 output's rounding leaves is written to out_lo, in bf16
+// too, so that the two together hold 16 bits of each value.
+template <bool B_MN, bool OUT_F32, bool SPLIT = false>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
                        const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2,
@@ -185,7 +182,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     bool ok = true;
     for (int t = cid; t < n_tiles && ok; t += n_pairs) {
       int tm, tn;
-      lin_tile(a, t, tm, tn);
+      lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
       const int ya = tm * kPairBM + static_cast<int>(rank) * kLinBM;
       const int yb = tn * a.bn + static_cast<int>(rank) * (a.bn / 2);
       for (int kb0 = 0; kb0 < a.kb_total; kb0 += kPairKps) {
@@ -300,7 +297,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     int it = 0;
     for (int t = cid; t < n_tiles; t += n_pairs, ++it) {
       int tm, tn;
-      lin_tile(a, t, tm, tn);
+      lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
       const int ab = it & 1;
       if (!mbar_wait_warp(&acc_full[ab], static_cast<uint32_t>((it >> 1) & 1), limit)) {
         if (lane == 0) lin_timeout(a.status, abort_flag);
@@ -310,39 +307,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const long long row = static_cast<long long>(tm) * kPairBM + rank * kLinBM + q * 32 + lane;
       const bool row_ok = row < a.M;
       const float rscale = (row_ok && a.rs_num) ? __ldg(a.rs_num + row) / __ldg(a.rs_den + row) : 1.f;
-      uint32_t top = 0;
-      float inv = 0.f;
 #pragma unroll 1
       for (int c = 0; c < a.bn / 32; ++c) {
         const int col0 = tn * a.bn + c * 32;
         if (col0 >= a.N) break;  // warp-uniform
         float v[32];
-        if (CKPT && c % 4 == 0) {
-          // columns past N are zeros (zero-filled operands): they do not count
-          top = 0;
-#pragma unroll 1
-          for (int cc = c; cc < c + 4; ++cc) {
-            tmem_ld32(tmem_lane + static_cast<uint32_t>(ab * kPairBN + cc * 32), v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top = max(top, abs_bits(v[e]));
-          }
-          inv = top_inverse(top);
-          if (row_ok) a.z_scale[row * ((a.N + 127) / 128) + col0 / 128] = top_scale(top);
-        }
         tmem_ld32(tmem_lane + static_cast<uint32_t>(ab * kPairBN + c * 32), v);
-        if (CKPT) {
-          int8_t* z_row = a.z8 + row * a.ldo;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float z[8];
-            uint32_t qc[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = v[8 * j + e];
-            codes_of<8>(z, top, inv, qc);
-            if (row_ok && col0 + 8 * j < a.N) CodeIO<8>::store(z_row + col0 + 8 * j, qc);
-          }
-          __syncwarp();
-        }
         const int my_col = col0 + lane;
         float gl = 0.f, bl = 0.f;
         if (my_col < a.N) {
@@ -371,6 +341,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 pk.z = pack_bf16x2(v[8 * j + 4], v[8 * j + 5]);
                 pk.w = pack_bf16x2(v[8 * j + 6], v[8 * j + 7]);
                 *reinterpret_cast<uint4*>(dst_row + col0 + 8 * j) = pk;
+                if (SPLIT) {
+                  uint4 lo;
+                  lo.x = pack_bf16x2(v[8 * j + 0] - bf16_lo(pk.x), v[8 * j + 1] - bf16_hi(pk.x));
+                  lo.y = pack_bf16x2(v[8 * j + 2] - bf16_lo(pk.y), v[8 * j + 3] - bf16_hi(pk.y));
+                  lo.z = pack_bf16x2(v[8 * j + 4] - bf16_lo(pk.z), v[8 * j + 5] - bf16_hi(pk.z));
+                  lo.w = pack_bf16x2(v[8 * j + 6] - bf16_lo(pk.w), v[8 * j + 7] - bf16_hi(pk.w));
+                  *reinterpret_cast<uint4*>(a.out_lo + row * a.ldo + col0 + 8 * j) = lo;
+                }
               }
             }
           }

@@ -121,6 +121,7 @@ SIGNATURES = {
         ctypes.c_int,
         [_c_void_p] * 5 + [_f32, _i64, _i64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p],
     ),
+    "dora_fused_linear_fwd_ckpt8_workspace_size": (_size, [_i64, _i64]),
     "dora_fused_linear_fwd_ckpt8": (
         ctypes.c_int,
         [_c_void_p] * 7 + [_f32, _i64, _i64, _i64, _i64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
@@ -453,6 +454,10 @@ def dora_fused_linear_fwd(x, W, A, B, m, n, s: float, bias=None, y=None, workspa
     return _fused_linear("dora_fused_linear_fwd", x, W, A, B, m, n, s, bias, y, None, None, workspace, stream)
 
 
+def dora_fused_linear_fwd_ckpt8_workspace_size(tokens: int, r: int) -> int:
+    return int(lib().dora_fused_linear_fwd_ckpt8_workspace_size(tokens, r))
+
+
 def dora_fused_linear_fwd_ckpt8(x, W, A, B, m, n, s: float, bias=None, y=None, z8=None, z_scale=None, workspace=None,
                                 stream=None):
     """dora_fused_linear_fwd that keeps z = x W^T + s * (x A^T) B^T for the backward: (y, z8, z_scale).
@@ -485,9 +490,9 @@ def _fused_linear(where, x, W, A, B, m, n, s, bias, y, z8, z_scale, workspace, s
     _dense_cuda(x, W, A, B, m, n, bias, y, z8, z_scale, workspace)
     if y is None:
         y = torch.empty(T, d_out, dtype=torch.bfloat16, device=x.device)
-    need = dora_fused_linear_fwd_workspace_size(T, r)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        size = dora_fused_linear_fwd_workspace_size if z8 is None else dora_fused_linear_fwd_ckpt8_workspace_size
+        workspace = torch.empty(size(T, r), dtype=torch.uint8, device=x.device)
     head = (_ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(bias), _ptr(m), _ptr(n), float(s), T, d_in, d_out, r, DORA_BF16,
             _ptr(y))
     tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))

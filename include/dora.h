@@ -400,11 +400,17 @@ DORA_API int dora_compose_fwd_ckpt8(const void* base_out, const void* lora_out, 
                                     const float* n, float s, int64_t tokens, int64_t d_out, dora_dtype dt, void* y,
                                     int8_t* z8, float* z_scale, void* stream);
 
+/* Bytes of workspace dora_fused_linear_fwd_ckpt8 needs: P as two [tokens, r]
+ * bf16 matrices (at least 512; none is read when r == 0). */
+DORA_API size_t dora_fused_linear_fwd_ckpt8_workspace_size(int64_t tokens, int64_t r);
+
 /* dora_fused_linear_fwd that also keeps z = x W^T + s (x A^T) B^T in 8 bits, as
- * dora_compose_fwd_ckpt8 does (z in fp32 as it leaves the product, before g and
- * b): the fused forward writes neither activation, so this is its training
- * form.  y is dora_fused_linear_fwd's arithmetic.  z8 16-byte aligned; the
- * rest, the workspace's size included, as there. */
+ * dora_compose_fwd_ckpt8 does (z in fp32, before g and b): the fused forward
+ * writes neither activation, so this is its training form.  P is kept in two
+ * bf16 halves and z summed in fp32 over chunks of K, so y and the scales are
+ * those of an fp32 product (y's last rounding apart).  z8 16-byte aligned;
+ * workspace at least dora_fused_linear_fwd_ckpt8_workspace_size() bytes; the
+ * rest as there. */
 DORA_API int dora_fused_linear_fwd_ckpt8(const void* x, const void* W, const void* A, const void* B, const void* bias,
                                          const float* m, const float* n, float s, int64_t tokens, int64_t d_in,
                                          int64_t d_out, int64_t r, dora_dtype dt, void* y, int8_t* z8, float* z_scale,

@@ -180,7 +180,8 @@ def test_fused_forward(T, d_in, d_out, r, bias):
     z = X @ Wd.T + Pm @ Bd.T
     low = np.abs(Pm) @ np.abs(Bd).T
     terms = np.abs(X) @ np.abs(Wd).T + low
-    p_err = d_in * E * s * (np.abs(X) @ np.abs(Ad).T) + U * np.abs(Pm)
+    # P in two bf16 halves: an fp32 sum, then twice a rounding to 8 bits
+    p_err = d_in * E * s * (np.abs(X) @ np.abs(Ad).T) + U * U * np.abs(Pm)
     err = p_err @ np.abs(Bd).T + (d_in + r) * E * terms
     zv = oracle.decode(z8.cpu().numpy(), zs.cpu().numpy(), 128)
     half = 0.5 * zs.cpu().double().numpy()[:, np.arange(d_out) // 128]
@@ -208,7 +209,7 @@ def test_training_step_captured_and_replayed():
     y, d_base, d_lora = (torch.empty(T, d_out, dtype=BF, device=DEV) for _ in range(3))
     z8, zs = torch.empty(T, d_out, dtype=torch.int8, device=DEV), torch.empty(T, 5, device=DEV)
     d_m = torch.empty(d_out, device=DEV)
-    ws_f = torch.empty(D.dora_fused_linear_fwd_workspace_size(T, r), dtype=torch.uint8, device=DEV)
+    ws_f = torch.empty(D.dora_fused_linear_fwd_ckpt8_workspace_size(T, r), dtype=torch.uint8, device=DEV)
     ws_b = torch.empty(D.dora_compose_bwd_ckpt8_workspace_size(T, d_out), dtype=torch.uint8, device=DEV)
 
     def step():
@@ -237,7 +238,7 @@ def test_training_step_captured_and_replayed():
         X = P.f64(x)
         Pm = s * (X @ P.f64(A).T)
         z = X @ P.f64(W).T + Pm @ P.f64(B).T
-        err = U * np.abs(Pm) @ np.abs(P.f64(B)).T + 2 * (d_in + r) * E * (
+        err = U * U * np.abs(Pm) @ np.abs(P.f64(B)).T + 2 * (d_in + r) * E * (
             np.abs(X) @ np.abs(P.f64(W)).T + s * np.abs(X) @ np.abs(P.f64(A)).T @ np.abs(P.f64(B)).T)
         half = 0.5 * zs.cpu().double().numpy()[:, np.arange(d_out) // 128]
         exact = np.sum(P.f64(dy) * z, axis=0) / P.f64(n)
@@ -269,3 +270,23 @@ def test_offsets_past_32_bits():
     v = D.dora_dequantize_i8(z8, zs)
     torch.cuda.synchronize()
     assert torch.equal(v[-16:], D.dora_dequantize_i8(z8[-16:].clone(), zs[-16:].clone()))
+
+
+def test_fused_scales_hold_fp32_over_a_long_k():
+    # the scales of z at K = 8192: an fp32 sum that rounds to nearest every 1024
+    # terms.  Within a chunk the tensor core's additions (of 16 products) drop
+    # bits, at most 2^-23 of the running sum each: 64 of them, and the running
+    # sum of a row that ends at its maximum is at most that of the magnitudes
+    T, K, N, r = 130, 8192, 384, 64
+    g = _gen(12)
+    x = torch.randn(T, K, generator=g).to(BF).to(DEV)
+    W = (0.015 * torch.randn(N, K, generator=g)).to(BF).to(DEV)
+    A = ((2 * torch.rand(r, K, generator=g) - 1) / K ** 0.5).to(BF).to(DEV)
+    B = (0.02 * torch.randn(N, r, generator=g)).to(BF).to(DEV)
+    one = torch.ones(N, device=DEV)
+    _, _, zs = D.dora_fused_linear_fwd_ckpt8(x, W, A, B, one, one, 0.5)
+    torch.cuda.synchronize()
+    z = P.f64(x) @ P.f64(W).T + 0.5 * (P.f64(x) @ P.f64(A).T) @ P.f64(B).T
+    top = np.stack([np.max(np.abs(z[:, j:j + 128]), axis=1) for j in range(0, N, 128)], axis=1)
+    rel = np.linalg.norm(127 * zs.cpu().double().numpy() - top) / np.linalg.norm(top)
+    assert rel <= 64 * 2.0 ** -23, rel

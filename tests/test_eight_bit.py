@@ -240,7 +240,7 @@ INV, UNS, WS, OK = D.DORA_ERR_INVALID_ARG, D.DORA_ERR_UNSUPPORTED, D.DORA_ERR_WO
         (dict(d_in=72), UNS), (dict(d_in=0), UNS), (dict(d_out=60), UNS), (dict(r=12), UNS), (dict(d_in=131072), UNS),
         (dict(x_q=ODD), UNS), (dict(W_q=ODD), UNS), (dict(y=ODD), UNS), (dict(x=ODD), UNS), (dict(B=ODD), UNS),
         (dict(x_scale=ODD), UNS), (dict(m=ODD), UNS), (dict(bias=ctypes.c_void_p(0x10001)), UNS),
-        (dict(workspace=None), WS), (dict(bytes=4 * 16 * 2 - 1), WS), (dict(workspace=ODD), UNS),
+        (dict(workspace=None), WS), (dict(bytes=255), WS), (dict(workspace=ODD), UNS),
         (dict(tokens=0), OK), (dict(d_out=0), OK)]),
     ("dora_compose_fwd_ckpt8", FWD, FWD_OK, [
         (dict(base=None), INV), (dict(z8=None), INV), (dict(z_scale=None), INV), (dict(tokens=-1), INV),
