@@ -22,6 +22,7 @@
 #include "compose.cuh"
 #include "linear_ckpt8.cuh"
 #include "linear_i8.cuh"
+#include "linear_slice.cuh"
 #include "linear_tc.cuh"
 #include "norm_bwd.cuh"
 #include "norm_simt.cuh"
@@ -70,6 +71,16 @@ int linear_i8_stages(int smem_optin) {
 size_t linear_i8_smem(int smem_optin) {
   return static_cast<size_t>(linear_i8_stages(smem_optin)) * kPairStageBytes + 1024 + kI8ColBytes + kI8BarrierBytes;
 }
+
+typedef void (*SliceKernel)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, SliceArgs);
+template <bool I8>
+SliceKernel slice_kernel(int bn) {
+  return bn == 16   ? linear_slice_kernel<I8, 16>
+         : bn == 32 ? linear_slice_kernel<I8, 32>
+         : bn == 64 ? linear_slice_kernel<I8, 64>
+                    : linear_slice_kernel<I8, 128>;
+}
+SliceKernel slice_kernel(bool i8, int bn) { return i8 ? slice_kernel<true>(bn) : slice_kernel<false>(bn); }
 
 template <typename K>
 int pair_attrs(K kernel, int smem_optin) {
@@ -161,6 +172,13 @@ int device_info(DeviceInfo** out) {
         pair_attrs(linear_pair_kernel<false, false, true>, d.smem_optin) ||
         pair_attrs(linear_i8_pair_kernel, d.smem_optin) || pair_attrs(linear_ckpt8_pair_kernel, d.smem_optin))
       return DORA_ERR_CUDA;
+    for (int i8 = 0; i8 < 2; ++i8)
+      for (int bn : {16, 32, 64, 128})
+        if (cudaFuncSetAttribute(slice_kernel(i8 != 0, bn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kSlSmem)) != cudaSuccess ||
+            cudaFuncSetAttribute(slice_kernel(i8 != 0, bn), cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+          return DORA_ERR_CUDA;
     {
       cudaLaunchConfig_t occ{};
       cudaLaunchAttribute cl[1];
@@ -927,6 +945,41 @@ int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, _
              : DORA_ERR_CUDA;
 }
 
+// Up to this many tokens the int8 linear runs on slices of the weight.
+constexpr int64_t kSliceTokens = 128;
+
+// Token tile of the slice kernels.
+int slice_bn(int64_t tokens) { return tokens <= 16 ? 16 : (tokens <= 32 ? 32 : (tokens <= 64 ? 64 : 128)); }
+
+// One slice launch over `a`: K split over as many CTAs of a cluster as keep
+// the grid within two CTAs an SM.
+int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const CUtensorMap& tmB,
+                 const CUtensorMap& tmP, SliceArgs a, bool after, const DeviceInfo* dev, cudaStream_t st) {
+  const int bn = slice_bn(a.tokens);
+  const long long row_tiles = cdiv(a.rows, kLinBM), tok_tiles = cdiv(a.tokens, bn);
+  int splits = 1;
+  while (splits < 8 && 2 * splits <= a.kb_main && row_tiles * tok_tiles * splits <= dev->num_sms) splits *= 2;
+  a.wait_limit = kWaitLimitCycles;
+  a.status = dev->status;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attrs[0].val.clusterDim.y = 1;
+  attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  cfg.attrs = attrs;
+  cfg.numAttrs = after ? 2 : 1;
+  cfg.blockDim = dim3(kSlThreads);
+  cfg.dynamicSmemBytes = kSlSmem;
+  cfg.gridDim = dim3(static_cast<unsigned>(row_tiles * splits), static_cast<unsigned>(tok_tiles));
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, slice_kernel(i8, bn), tmW, tmX, tmB, tmP, a) == cudaSuccess ? DORA_OK
+                                                                                               : DORA_ERR_CUDA;
+}
+
 int fused_linear(const void* x, const void* W, const void* A, const void* B, const void* bias, const float* m,
                  const float* n, float s, int64_t tokens, int64_t d_in, int64_t d_out, int64_t r, dora_dtype dt,
                  void* y, bool ckpt, int8_t* z8, float* z_scale, void* workspace, size_t workspace_bytes,
@@ -1227,6 +1280,32 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* P = static_cast<__nv_bfloat16*>(workspace);
   CUtensorMap tmXq, tmWq, tmX, tmA, tmP, tmB;
+  if (tokens <= kSliceTokens) {
+    const uint32_t bn = slice_bn(tokens);
+    if (make_map_i8(&tmWq, W_q, d_out, d_in, kLinBM) || make_map_i8(&tmXq, x_q, tokens, d_in, bn)) return DORA_ERR_CUDA;
+    SliceArgs sa{};
+    sa.tokens = static_cast<int>(tokens);
+    if (r > 0) {
+      if (make_map(&tmA, A, r, d_in) || make_map(&tmX, x, tokens, d_in, bn) || make_map(&tmB, B, d_out, r) ||
+          make_map(&tmP, P, tokens, r, bn))
+        return DORA_ERR_CUDA;
+      sa.rows = static_cast<int>(r);
+      sa.kb_main = sa.kb_total = static_cast<int>(cdiv(d_in, kLinBK));
+      sa.alpha = s;
+      sa.out = P;
+      if (launch_slice(false, tmA, tmX, tmA, tmX, sa, false, dev, st)) return DORA_ERR_CUDA;
+    }
+    sa.rows = static_cast<int>(d_out);
+    sa.kb_main = static_cast<int>(cdiv(d_in, kI8BK));
+    sa.kb_total = sa.kb_main + static_cast<int>(cdiv(r, kLinBK));
+    sa.x_scale = x_scale;
+    sa.w_scale = w_scale;
+    sa.m = m;
+    sa.n = n;
+    sa.bias = static_cast<const __nv_bfloat16*>(bias);
+    sa.out = static_cast<__nv_bfloat16*>(y);
+    return launch_slice(true, tmWq, tmXq, r > 0 ? tmB : tmWq, r > 0 ? tmP : tmXq, sa, r > 0, dev, st);
+  }
   if (make_map_i8(&tmXq, x_q, tokens, d_in, kLinBM) || make_map_i8(&tmWq, W_q, d_out, d_in, kPairBN / 2))
     return DORA_ERR_CUDA;
   if (r > 0) {

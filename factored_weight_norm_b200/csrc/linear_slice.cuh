@@ -1,0 +1,299 @@
+// linear_slice.cuh - the int8 DoRA linear and its adapter's down projection
+// for few tokens, on tcgen05 tensor cores (sm_100a).
+//
+// With few tokens the product reads the whole weight for little arithmetic:
+// it is bound by memory, and what matters is that every SM streams.  So the
+// weight's rows are the MMA's M side (128 of them a tile) and the tokens its N
+// side (BN = 16 to 128 of them), and K is split over a cluster of up to 8 CTAs
+// until the grid fills two CTAs an SM; each CTA streams its slice of 128
+// weight rows through a ring of TMA boxes (about 100 KB in flight).  The
+// splits meet in distributed shared memory: each CTA puts its partial tile
+// into its own (the ring is free by then), and each finishes its share of the
+// tokens from all of them.  int32 partial sums are exact in any order; the
+// adapter's product lies wholly in the last split, so its fp32 sum is one
+// CTA's; the fp32 sums of the down projection are added in split order.
+#pragma once
+
+#include "linear_i8.cuh"
+
+namespace dora {
+
+constexpr int kSlThreads = 192;  // producer, MMA issuer, four epilogue warps
+constexpr int kSlChunk = 64;     // tokens exchanged at a time
+constexpr int kSlMaxStages = 8;
+constexpr size_t kSlSmem = 112 * 1024;  // two CTAs on an SM
+constexpr size_t kSlFixed = 1024 + 256; // alignment, barriers
+
+__host__ __device__ constexpr uint32_t slice_stage_bytes(int bn) { return kLinABytes + bn * 128u; }
+__host__ __device__ constexpr int slice_stages(int bn) {
+  const int n = static_cast<int>((kSlSmem - kSlFixed) / slice_stage_bytes(bn));
+  return n < kSlMaxStages ? n : kSlMaxStages;
+}
+
+struct SliceArgs {
+  int rows;               // weight rows (d_out; r for the down projection)
+  int tokens;
+  int kb_main, kb_total;  // K blocks; total with the adapter's
+  const float* x_scale;   // I8: as in LinearI8Args
+  const float* w_scale;
+  const float* m;
+  const float* n;
+  const __nv_bfloat16* bias;
+  float alpha;            // !I8: scale of the product
+  __nv_bfloat16* out;     // [tokens, rows]
+  long long wait_limit;
+  int* status;
+};
+
+// First K block of split i of `splits`: even shares of all blocks, but every
+// split keeps a main block and the adapter's blocks all go to the last.
+__device__ __forceinline__ int slice_start(const SliceArgs& a, int i, int splits) {
+  if (i == splits) return a.kb_total;
+  return min(static_cast<int>(static_cast<long long>(a.kb_total) * i / splits), a.kb_main - (splits - i));
+}
+
+__device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, signed 8-bit operands, int32 accumulation.
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                      uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// I8: out = bf16(b + g * (sx sw * (W_q x_q^T) + B P^T)), tmW/tmX int8 and
+// tmB/tmP the adapter's; else out = bf16(alpha * W x^T), all bf16.
+template <bool I8, int BN>
+__global__ void __launch_bounds__(kSlThreads)
+    linear_slice_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                        const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmP,
+                        const SliceArgs a) {
+  constexpr int kStages = slice_stages(BN);
+  constexpr uint32_t kStageBytes = slice_stage_bytes(BN);
+  constexpr int kCh = BN < kSlChunk ? BN : kSlChunk;
+  constexpr uint32_t kColsTmem = I8 ? 2 * BN : (BN < 32 ? 32 : BN);
+  static_assert(kStages * kStageBytes >= 2 * kCh * 512, "the exchange fits in the ring");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_s = smem_u32(smem_raw);
+  const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base_s - raw_s);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  uint32_t splits;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
+  const uint32_t rank = cluster_ctarank();
+  const int row0 = static_cast<int>(blockIdx.x / splits) * kLinBM;
+  const int tok0 = static_cast<int>(blockIdx.y) * BN;
+  const int kb0 = slice_start(a, static_cast<int>(rank), static_cast<int>(splits));
+  const int kb1 = slice_start(a, static_cast<int>(rank) + 1, static_cast<int>(splits));
+  const bool has_ext = I8 && kb1 > a.kb_main;
+  const long long limit = a.wait_limit;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kColsTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_launch();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int filled = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++filled) {
+        const int s = filled % kStages;
+        const bool ext = I8 && kb >= a.kb_main;
+        if (ext && kb == a.kb_main) {
+          grid_dep_wait();  // P comes from the launch before
+          fence_proxy_async_all();
+        }
+        if (!mbar_wait(&empty[s], static_cast<uint32_t>(filled / kStages & 1) ^ 1u, limit)) {
+          atomicExch(a.status, 5);  // DORA_ERR_TIMEOUT
+          break;
+        }
+        mbar_arrive_expect_tx(&full[s], kStageBytes);
+        const int xk = I8 && !ext ? kb * kI8BK : (ext ? kb - a.kb_main : kb) * kLinBK;
+        tma_load_2d(base_s + s * kStageBytes, ext ? &tmB : &tmW, &full[s], xk, row0);
+        tma_load_2d(base_s + s * kStageBytes + kLinABytes, ext ? &tmP : &tmX, &full[s], xk, tok0);
+      }
+      // never leave a TMA copy in flight: the last fill of every stage
+      for (int f = max(0, filled - kStages); f < filled; ++f)
+        mbar_wait(&full[f % kStages], static_cast<uint32_t>(f / kStages & 1), limit);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_m = I8 ? idesc_i8_s32(kLinBM, BN) : idesc_bf16_f32(kLinBM, BN);
+      const uint32_t idesc_e = idesc_bf16_f32(kLinBM, BN);
+      const uint64_t desc0 = sw128_kmajor_desc(base_s);
+      bool ok = true;
+      int it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int s = it % kStages;
+        if (!mbar_wait(&full[s], static_cast<uint32_t>(it / kStages & 1), limit)) {
+          atomicExch(a.status, 5);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t ad = desc0 + static_cast<uint64_t>(s) * (kStageBytes >> 4);
+        const uint64_t bd = ad + (kLinABytes >> 4);
+        const bool ext = I8 && kb >= a.kb_main;
+        const uint32_t first = ext ? a.kb_main : kb0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t acc = (kb > static_cast<int>(first) || k > 0) ? 1u : 0u;
+          if (ext)
+            mma_bf16(tmem + BN, ad + 2 * k, bd + 2 * k, idesc_e, acc);
+          else if (I8)
+            mma_i8(tmem, ad + 2 * k, bd + 2 * k, idesc_m, acc);
+          else
+            mma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc_m, acc);
+        }
+        mma_commit(&empty[s]);
+      }
+      // after a wait that gave up the MMAs already issued must still end before TMEM is freed
+      mma_commit(acc_full);
+      if (!ok) mbar_wait(acc_full, 0, limit);
+    }
+  }
+  __syncwarp();
+
+  // ---------------------------------------------------------------- exchange
+  const int et = static_cast<int>(threadIdx.x) - 64;  // epilogue thread
+  const int group = (et & 15) * 8;                    // its eight rows of the tile
+  const bool group_ok = et >= 0 && row0 + group < a.rows;
+  float g[8], sw[8], b[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    g[e] = 1.f;
+    sw[e] = b[e] = 0.f;
+    if (I8 && group_ok) {
+      const int c = row0 + group + e;
+      g[e] = a.m ? __ldg(a.m + c) / __ldg(a.n + c) : 1.f;
+      sw[e] = __ldg(a.w_scale + c) * g[e];
+      if (a.bias) b[e] = __bfloat162float(a.bias[c]);
+    }
+  }
+  bool alive = true;
+  if (et >= 0) {
+    alive = mbar_wait_warp(acc_full, 0, limit);
+    if (!alive && lane == 0) atomicExch(a.status, 5);
+    tc_fence_after();
+  }
+  const int q = warp & 3;
+  const bool ext_any = I8 && a.kb_total > a.kb_main;
+#pragma unroll 1
+  for (int c0 = 0; c0 < BN; c0 += kCh) {
+    if (tok0 + c0 >= a.tokens) break;  // the same for the whole cluster
+    if (et >= 0 && alive) {
+      const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + c0;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(smem) + q * 32 + lane;
+#pragma unroll
+      for (int j = 0; j < kCh; j += 16) {
+        uint32_t u[16];
+        tmem_ld16(lane_addr + j, u);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dst[(j + e) * 128] = u[e];
+        if (has_ext) {
+          tmem_ld16(lane_addr + BN + j, u);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) dst[(kCh + j + e) * 128] = u[e];
+        }
+      }
+    }
+    cluster_sync_all();
+    if (group_ok) {
+      for (int i = et >> 4; i * static_cast<int>(splits) + static_cast<int>(rank) < kCh; i += 8) {
+        const int j = i * static_cast<int>(splits) + static_cast<int>(rank);
+        const int t = tok0 + c0 + j;
+        if (t >= a.tokens) break;
+        const uint32_t at = base_s + static_cast<uint32_t>(j) * 512u + static_cast<uint32_t>(group) * 4u;
+        float o[8];
+        if (I8) {
+          int sum[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] = 0;
+          for (uint32_t p = 0; p < splits; ++p) {
+            const uint32_t from = mapa_shared(at, p);
+            const uint4 x = ld_cluster_u4(from), y = ld_cluster_u4(from + 16);
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += static_cast<int>(w[e]);
+          }
+          const float sx = __ldg(a.x_scale + t);
+          float low[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) low[e] = b[e];
+          if (ext_any) {
+            const uint32_t from = mapa_shared(at + kCh * 512u, splits - 1);
+            const uint4 x = ld_cluster_u4(from), y = ld_cluster_u4(from + 16);
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) low[e] = fmaf(g[e], __uint_as_float(w[e]), b[e]);
+          }
+          // as linear_i8_pair_kernel's epilogue, operation by operation
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(static_cast<float>(sum[e]) * sx, sw[e], low[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = 0.f;
+          for (uint32_t p = 0; p < splits; ++p) {
+            const uint32_t from = mapa_shared(at, p);
+            const uint4 x = ld_cluster_u4(from), y = ld_cluster_u4(from + 16);
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += __uint_as_float(w[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] *= a.alpha;
+        }
+        uint4 pk;
+        pk.x = pack_bf16x2(o[0], o[1]);
+        pk.y = pack_bf16x2(o[2], o[3]);
+        pk.z = pack_bf16x2(o[4], o[5]);
+        pk.w = pack_bf16x2(o[6], o[7]);
+        *reinterpret_cast<uint4*>(a.out + static_cast<long long>(t) * a.rows + row0 + group) = pk;
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // the next chunk, or the end, may not overtake a reader of this CTA's memory
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kColsTmem);
+}
+
+}  // namespace dora
