@@ -25,7 +25,7 @@
 
 namespace dora {
 
-constexpr int kCkChunk = 4;  // ring stages (of two 64-deep K blocks) summed in TMEM at a time
+constexpr int kCkChunk = 6;  // ring stages (of two 64-deep K blocks) summed in TMEM at a time
 
 struct LinearCkptArgs {
   int M, N;
