@@ -259,9 +259,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       const int col0 = tn * kPairBN + half * 128;
       if (alive && row < a.M && col0 < a.N) {
         // columns past N are sums of zero-filled operands: they do not count
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 128; ++e) top = max(top, abs_bits(v[e]));
+        const uint32_t top = __float_as_uint(max_abs<128>(0.f, v));
         const float inv = top_inverse(top);
         a.z_scale[row * blocks + col0 / kCkptBlock] = top_scale(top);
         const float* gv = cf + half * 128;

@@ -5,10 +5,10 @@
 // codes q with one fp32 scale:
 //   top = max |v|,  scale = top / 127,  q = 127 v / top rounded to the nearest
 //   integer, ties to even;  the value that is kept is q * scale.
-// q is the rounding of the exact quotient, whatever the arithmetic: the fp32
-// product v * (127 / top) is off by at most 127 * 2^-23, and a product that
-// lands within kTieBand of a half is rounded again in fp64 (127 v is exact
-// there, and an fp64 quotient cannot cross a half that an fp32 ratio missed).
+// q is the rounding of the exact quotient, whatever the arithmetic: v * (127 /
+// top) in one fused rounding is off by at most 127 * 2^-24 (the factor's own
+// rounding), and a product that lands within kTieBand of a half is decided by
+// exact arithmetic (codes_settle).
 // A stretch below 2^-100 everywhere keeps zeros and the scale 0 (127 / top
 // would leave fp32's range); one that holds an infinity or a NaN keeps the
 // scale NaN, so that its values come back as NaN and not as numbers.
@@ -21,13 +21,10 @@ namespace dora {
 constexpr int kCkptBlock = 128;              // columns of a token that share a scale in a checkpoint
 constexpr uint32_t kTopTiny = 0x0D800000u;   // 2^-100
 constexpr uint32_t kTopInf = 0x7F800000u;
-constexpr float kTieBand = 3e-5f;            // above 127 * 2^-23
+constexpr float kTieBand = 1e-5f;            // above 127 * 2^-24
 constexpr float kRoundMagic = 12582912.f;    // 1.5 * 2^23: x + magic rounds x to an integer in the low bits
 
-// |v| as bits: ordered as unsigned integers, NaN above infinity, so that an
-// integer maximum never loses one.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
+// A maximum is kept as |v|'s bits: ordered as unsigned integers, NaN above infinity.
 __device__ __forceinline__ bool top_kept(uint32_t top) { return top >= kTopTiny && top < kTopInf; }
 
 __device__ __forceinline__ float top_inverse(uint32_t top) {
@@ -38,31 +35,94 @@ __device__ __forceinline__ float top_scale(uint32_t top) {
   return top_kept(top) ? __uint_as_float(top) / 127.f : (top >= kTopInf ? __uint_as_float(0x7FC00000u) : 0.f);
 }
 
-// Codes of E values that share (top, inv), one in the low byte of each word.
-// Values of a stretch that keeps no codes (inv == 0) give zeros.
+// max(a, |b|, |c|) that keeps a NaN: its bits are then above infinity's.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 template <int E>
-__device__ __forceinline__ void codes_of(const float (&v)[E], uint32_t top, float inv, uint32_t (&q)[E]) {
-  bool near = false;
+__device__ __forceinline__ float max_abs(float a, const float (&v)[E]) {
+  if constexpr (E == 1) {
+    return max_abs(a, v[0], v[0]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) a = max_abs(a, v[e], v[e + 1]);
+    return a;
+  }
+}
+
+// Codes of E values by inv = 127 / top, one in the low byte of each word;
+// returns whether they are settled: not so if one of them lies too near a half
+// for fp32 (inv is off by 2^-24 of itself, and each product meets one
+// rounding) or is no number.
+template <int E>
+__device__ __forceinline__ bool codes_fast(const float (&v)[E], float inv, uint32_t (&q)[E]) {
+  float rest[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const float r = fmaf(v[e], inv, kRoundMagic);
     q[e] = __float_as_uint(r);
-    near = near || fabsf(fmaf(v[e], inv, -(r - kRoundMagic))) > 0.5f - kTieBand;
+    rest[e] = fmaf(v[e], inv, kRoundMagic - r);
   }
-  if (inv == 0.f) {
+  return max_abs<E>(0.f, rest) <= 0.5f - kTieBand;
+}
+
+// Settles the codes that codes_fast left open.  A product near the half
+// h = k +- 1/2 is decided by the sign of 127 v - h top, which two-term products
+// give exactly: a product's rounding error is a float (an fma finds it), the
+// two leading terms are within a factor of two, so that their difference is
+// exact, and the errors' difference has few enough bits to be exact as well.
+// bf16 rows meet this often: their values are few, and v = top / 2 is a tie
+// (one value in a thousand of a normal row), so it has to be cheap.
+template <int E>
+__device__ __forceinline__ void codes_settle(const float (&v)[E], uint32_t top, float inv, uint32_t (&q)[E]) {
+  if (!top_kept(top)) {
 #pragma unroll
     for (int e = 0; e < E; ++e) q[e] = 0;
-  } else if (near) {  // about one value in 10^4
-    const double d = static_cast<double>(__uint_as_float(top));
-#pragma unroll 1
-    for (int e = 0; e < E; ++e) {
-      float ve = 0.f;
+    return;
+  }
+  float t = __uint_as_float(top);
+  const float scale = t > 0x1p64f ? 0x1p-64f : 1.f;  // keeps 127 v in range; exact
+  t *= scale;
 #pragma unroll
-      for (int k = 0; k < E; ++k) ve = k == e ? v[k] : ve;
-      const uint32_t qe = static_cast<uint32_t>(__double2int_rn(127.0 * static_cast<double>(ve) / d));
-#pragma unroll
-      for (int k = 0; k < E; ++k) q[k] = k == e ? qe : q[k];
+  for (int e = 0; e < E; ++e) {
+    const float k = __uint_as_float(q[e]) - kRoundMagic;
+    const float d = fmaf(v[e], inv, -k);
+    if (fabsf(d) > 0.5f - kTieBand) {
+      const float x = v[e] * scale, h = k + copysignf(0.5f, d);
+      const float hi = 127.f * x, hh = h * t;
+      const float past = copysignf(1.f, d) * ((hi - hh) + (fmaf(127.f, x, -hi) - fmaf(h, t, -hh)));
+      if (past > 0.f || (past == 0.f && (q[e] & 1u))) q[e] += d > 0.f ? 1u : ~0u;
     }
+  }
+}
+
+// Codes of E values that share (top, inv).
+template <int E>
+__device__ __forceinline__ void codes_of(const float (&v)[E], uint32_t top, float inv, uint32_t (&q)[E]) {
+  if (!codes_fast<E>(v, inv, q)) codes_settle<E>(v, top, inv, q);
+}
+
+// Codes of bf16 values that share (top, inv): with 8 bits of v, 127 v / 256 is
+// exact, so that one step of Markstein's correction (the quotient plus its
+// exact remainder times the reciprocal; IBM J. Res. Dev. 34(1), 1990) gives the
+// rounded quotient itself: a tie stays a tie and no other quotient of two bf16
+// numbers is near one.  Without branches: ties are common here (v = top / 2 is
+// one; one value in a thousand of a normal row), and settling them one by one
+// took 91 us instead of 80.5 for 27648 rows of 5120.
+template <int E>
+__device__ __forceinline__ void codes_of_bf16(const float (&v)[E], uint32_t top, float inv, uint32_t (&q)[E]) {
+  const bool kept = top_kept(top);
+  const float t = __uint_as_float(top) * 0x1p-8f, back = kept ? 1.f / t : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float q0 = v[e] * inv;
+    q[e] = __float_as_uint(fmaf(fmaf(-q0, t, v[e] * (127.f * 0x1p-8f)), back, q0) + kRoundMagic);
+  }
+  if (!kept) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) q[e] = 0;
   }
 }
 
@@ -145,22 +205,34 @@ struct RowsI8Args {
   float eps;
 };
 
-// (sum, maximum) over the CTA, the same bits in every thread.
-__device__ __forceinline__ void rows_i8_reduce(float& sum, uint32_t& top, float* s_sum, uint32_t* s_top) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+// (sum, maximum) over the `warps` warps that meet at barrier `bar`, the same
+// bits in every thread: each warp leaves its own in shared memory and every
+// thread adds them in order (a second round of shuffles would take longer).
+struct RowsI8Shared {
+  float sum[32];
+  uint32_t top[32];
+};
+__device__ __forceinline__ void rows_i8_reduce(float& sum, uint32_t& top, RowsI8Shared& sh, int warps, int bar) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) {
-    s_sum[warp] = sum;
-    s_top[warp] = top;
+    sh.sum[warp] = sum;
+    sh.top[warp] = top;
   }
-  __syncthreads();
-  sum = lane < warps ? s_sum[lane] : 0.f;
-  top = lane < warps ? s_top[lane] : 0u;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  top = __reduce_max_sync(0xffffffffu, top);
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
+  top = __reduce_max_sync(0xffffffffu, lane < warps ? sh.top[lane] : 0u);
+  float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int w = 0; w < warps; w += 4) {
+    const float4 p = *reinterpret_cast<const float4*>(&sh.sum[w]);
+    s4[0] += p.x;
+    if (w + 1 < warps) s4[1] += p.y;
+    if (w + 2 < warps) s4[2] += p.z;
+    if (w + 3 < warps) s4[3] += p.w;
+  }
+  sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
 }
 
 // The row's factor 1 / sqrt(mean + eps); NaN where the squares left fp32's
@@ -170,78 +242,105 @@ __device__ __forceinline__ float rows_i8_rstd(float sum, long long d, float eps)
   return ms < __uint_as_float(kTopInf) ? 1.f / sqrtf(ms + eps) : __uint_as_float(0x7FC00000u);
 }
 
-// NV vectors of VEC columns per thread, the row kept in registers.
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(1024) rows_i8_kernel(const RowsI8Args a) {
-  __shared__ float s_sum[32];
-  __shared__ uint32_t s_top[32];
-  const long long row = blockIdx.x;
-  const T* x = static_cast<const T*>(a.x) + row * a.d;
-  const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.d : nullptr;
-  const T* w = static_cast<const T*>(a.weight);
+// One row in a thread's registers: NV vectors of VEC columns, `stride` columns
+// apart.  All of a row's steps are written without branches (columns past the
+// end are zeros that are not stored), so that the vectors overlap.
+template <typename T, int VEC, int NV, bool HAS_W>
+struct RowI8 {
+  using IO = VecIO<T, VEC>;
+  using Raw = typename IO::Raw;
   float v[NV][VEC];
-  float sum = 0.f;
-  uint32_t top = 0;
+  float sum, top;
+
+  // h = x + residual (stored), v = h * w, and this thread's share of the sums
+  __device__ __forceinline__ void take(const Raw (&x)[NV], const Raw (&r)[NV], const Raw (&w)[NV], bool has_res, T* h, int col, int stride, int d) {
+    sum = top = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const long long col = (static_cast<long long>(i) * blockDim.x + threadIdx.x) * VEC;
+    for (int i = 0; i < NV; ++i) {
+      IO::unpack(x[i], v[i]);
+      if (has_res) {
+        float f[VEC];
+        IO::unpack(r[i], f);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-    if (col < a.d) {
-      VecIO<T, VEC>::unpack(VecIO<T, VEC>::raw(x + col), v[i]);
-      if (res) {
-        float r[VEC];
-        VecIO<T, VEC>::unpack(VecIO<T, VEC>::raw(res + col), r);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] = round_to(v[i][e] + r[e], x);
-        VecIO<T, VEC>::store(static_cast<T*>(a.h) + row * a.d + col, v[i]);
+        for (int e = 0; e < VEC; ++e) v[i][e] = round_to(v[i][e] + f[e], h);
+        if (col + i * stride < d) IO::store(h + col + i * stride, v[i]);
       }
-      if (w) {
-        float ww[VEC];
-        VecIO<T, VEC>::unpack(VecIO<T, VEC>::raw_param(w + col), ww);
+      if (HAS_W) {
+        float f[VEC];
+        IO::unpack(w[i], f);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           sum = fmaf(v[i][e], v[i][e], sum);
-          v[i][e] *= ww[e];
+          v[i][e] *= f[e];
         }
       }
+      top = max_abs<VEC>(top, v[i]);
     }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) top = max(top, abs_bits(v[i][e]));
   }
-  rows_i8_reduce(sum, top, s_sum, s_top);
-  const float rstd = w ? rows_i8_rstd(sum, a.d, a.eps) : 1.f;
-  const float inv = top_inverse(top);
-  if (threadIdx.x == 0) a.scale[row] = top_scale(top) * rstd;
+
+  // codes by the row's maximum, and y
+  __device__ __forceinline__ void give(uint32_t row_top, float inv, float rstd, int8_t* q, T* y, int col, int stride,
+                                       int d) const {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const long long col = (static_cast<long long>(i) * blockDim.x + threadIdx.x) * VEC;
-    if (col < a.d) {
-      uint32_t q[VEC];
-      codes_of<VEC>(v[i], top, inv, q);
-      CodeIO<VEC>::store(a.q + row * a.d + col, q);
-      if (a.y) {
+    for (int i = 0; i < NV; ++i) {
+      uint32_t c[VEC];
+      if constexpr (!HAS_W && sizeof(T) == 2)
+        codes_of_bf16<VEC>(v[i], row_top, inv, c);
+      else
+        codes_of<VEC>(v[i], row_top, inv, c);
+      if (col + i * stride < d) CodeIO<VEC>::store(q + col + i * stride, c);
+    }
+    if (y) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] *= rstd;
-        VecIO<T, VEC>::store(static_cast<T*>(a.y) + row * a.d + col, v[i]);
+      for (int i = 0; i < NV; ++i) {
+        float o[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = v[i][e] * rstd;
+        if (col + i * stride < d) IO::store(y + col + i * stride, o);
       }
     }
   }
+};
+
+// One CTA of at most MAXT threads per row, the row in registers.
+template <typename T, int VEC, int NV, int MAXT, bool HAS_W>
+__global__ void __launch_bounds__(MAXT) rows_i8_kernel(const RowsI8Args a) {
+  __shared__ __align__(16) RowsI8Shared sh;
+  using IO = VecIO<T, VEC>;
+  const long long off = static_cast<long long>(blockIdx.x) * a.d;
+  const int d = static_cast<int>(a.d), col = threadIdx.x * VEC, stride = blockDim.x * VEC;
+  const bool has_res = a.residual != nullptr;
+  typename IO::Raw x[NV], r[NV], w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    x[i] = r[i] = w[i] = typename IO::Raw{};
+    if (col + i * stride < d) {
+      x[i] = IO::raw(static_cast<const T*>(a.x) + off + col + i * stride);
+      if (has_res) r[i] = IO::raw(static_cast<const T*>(a.residual) + off + col + i * stride);
+      if (HAS_W) w[i] = IO::raw_param(static_cast<const T*>(a.weight) + col + i * stride);
+    }
+  }
+  RowI8<T, VEC, NV, HAS_W> row;
+  row.take(x, r, w, has_res, static_cast<T*>(a.h) + off, col, stride, d);
+  float sum = row.sum;
+  uint32_t top = __float_as_uint(row.top);
+  rows_i8_reduce(sum, top, sh, blockDim.x >> 5, 0);
+  const float rstd = HAS_W ? rows_i8_rstd(sum, a.d, a.eps) : 1.f;
+  if (threadIdx.x == 0) a.scale[blockIdx.x] = top_scale(top) * rstd;
+  row.give(top, top_inverse(top), rstd, a.q + off, a.y ? static_cast<T*>(a.y) + off : nullptr, col, stride, d);
 }
 
 // Rows longer than a CTA's registers hold: the row is read twice, the second
 // time as written (h) where there is a residual.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(1024) rows_i8_long_kernel(const RowsI8Args a) {
-  __shared__ float s_sum[32];
-  __shared__ uint32_t s_top[32];
+  __shared__ __align__(16) RowsI8Shared sh;
   const long long row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.d;
   const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.d : nullptr;
   const T* w = static_cast<const T*>(a.weight);
   T* h = static_cast<T*>(a.h) + row * a.d;
-  float sum = 0.f;
-  uint32_t top = 0;
+  float sum = 0.f, top_f = 0.f;
   for (long long col = static_cast<long long>(threadIdx.x) * VEC; col < a.d;
        col += static_cast<long long>(blockDim.x) * VEC) {
     float v[VEC];
@@ -262,10 +361,10 @@ __global__ void __launch_bounds__(1024) rows_i8_long_kernel(const RowsI8Args a) 
         v[e] *= ww[e];
       }
     }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) top = max(top, abs_bits(v[e]));
+    top_f = max_abs<VEC>(top_f, v);
   }
-  rows_i8_reduce(sum, top, s_sum, s_top);
+  uint32_t top = __float_as_uint(top_f);
+  rows_i8_reduce(sum, top, sh, blockDim.x >> 5, 0);
   const float rstd = w ? rows_i8_rstd(sum, a.d, a.eps) : 1.f;
   const float inv = top_inverse(top);
   if (threadIdx.x == 0) a.scale[row] = top_scale(top) * rstd;
@@ -301,40 +400,52 @@ __device__ __forceinline__ void st_value<float>(float* p, float v) { *p = v; }
 template <>
 __device__ __forceinline__ void st_value<__nv_bfloat16>(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <typename T, int VEC>
+// U rows of VEC neighbouring columns per thread and step, their loads issued
+// together; VEC fills one 16-byte store (8 bf16, 4 fp32), so that a warp's
+// stores are whole lines.  Measured at 8192 x 8192 to bf16 (201 MB): 31.7 us;
+// one row a step 36.2, and 16 codes a thread (two half-line stores) 41.
+template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) dequant_i8_kernel(const int8_t* __restrict__ q, const float* __restrict__ scale,
                                                          long long rows, long long cols, long long block,
                                                          long long blocks, T* __restrict__ out) {
   const long long col = (blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x) * VEC;
   if (col >= cols) return;
-  const long long b = col / block;
-  for (long long row = blockIdx.y; row < rows; row += gridDim.y) {
-    const float sc = __ldg(scale + row * blocks + b);
-    const int8_t* src = q + row * cols + col;
-    T* dst = out + row * cols + col;
-    if constexpr (VEC == 8) {
-      const uint2 w = ld_stream_u2(src);
-      float v[8], u[4];
-      unpack_codes(w.x, u);
+  const float* sc0 = scale + col / block;
+  for (long long row = blockIdx.y * static_cast<long long>(U); row < rows; row += gridDim.y * static_cast<long long>(U)) {
+    float sc[U];
+    uint2 w[U];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = u[e] * sc;
-      unpack_codes(w.y, u);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 + e] = u[e] * sc;
-      if constexpr (sizeof(T) == 2) {
-        VecIO<T, 8>::store(dst, v);
-      } else {
-        float lo[4], hi[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          lo[e] = v[e];
-          hi[e] = v[4 + e];
-        }
-        VecIO<T, 4>::store(dst, lo);
-        VecIO<T, 4>::store(dst + 4, hi);
+    for (int u = 0; u < U; ++u) {
+      if (row + u < rows) {
+        const int8_t* src = q + (row + u) * cols + col;
+        sc[u] = __ldg(sc0 + (row + u) * blocks);
+        if constexpr (VEC == 8)
+          w[u] = ld_stream_u2(src);
+        else if constexpr (VEC == 4)
+          w[u].x = ld_stream_u1(src);
+        else
+          w[u].x = static_cast<uint32_t>(static_cast<int32_t>(__ldg(src)));
       }
-    } else {
-      st_value<T>(dst, static_cast<float>(src[0]) * sc);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (row + u < rows) {
+        T* dst = out + (row + u) * cols + col;
+        if constexpr (VEC == 1) {
+          st_value<T>(dst, static_cast<float>(static_cast<int32_t>(w[u].x)) * sc[u]);
+        } else {
+          float v[VEC], a[4];
+          unpack_codes(w[u].x, a);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = a[e] * sc[u];
+          if constexpr (VEC == 8) {
+            unpack_codes(w[u].y, a);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 + e] = a[e] * sc[u];
+          }
+          VecIO<T, VEC>::store(dst, v);
+        }
+      }
     }
   }
 }

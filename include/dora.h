@@ -356,7 +356,7 @@ DORA_API int dora_rms_norm_i8(const void* x, const void* residual, const void* w
 /* out[i, j] = q[i, j] * scale, rounded once to dt.  block = 0: scale is fp32
  * [rows]; block = 128: fp32 [rows, ceil(cols / 128)] (a checkpoint's); other
  * values are DORA_ERR_UNSUPPORTED.  Any width; q, out with their types'
- * alignment (16-byte aligned out and widths of 8 columns run fastest). */
+ * alignment (16-byte aligned out and widths of 8 columns (fp32: 4) run fastest). */
 DORA_API int dora_dequantize_i8(const int8_t* q, const float* scale, int64_t rows, int64_t cols, int64_t block,
                                 dora_dtype dt, void* out, void* stream);
 

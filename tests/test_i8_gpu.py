@@ -50,7 +50,8 @@ def _assert_within(got, ref, tol, what):
 # scalar fp32 rows, and rows longer than the registers of one CTA
 ROWS = [(1, 8, BF), (3, 264, BF), (1, 8192, BF), (400, 2048, BF), (301, 4096, BF), (300, 8192, BF), (297, 16384, BF),
         (2, 32768, BF), (2, 33000, BF), (1, 1, F32), (5, 33, F32), (2, 4099, F32), (300, 4099, F32), (300, 6000, F32),
-        (299, 1024, F32), (1, 8192, F32), (2, 33001, F32), (2, 40000, F32)]
+        (299, 1024, F32), (1, 8192, F32), (2, 33001, F32), (2, 40000, F32),
+        (2500, 4096, BF), (1300, 8192, BF), (1250, 8200, BF), (2400, 4104, F32), (700, 16384, BF), (1200, 8196, F32)]
 
 
 @pytest.mark.parametrize("rows, cols, dtype", ROWS, ids=lambda v: str(v).replace("torch.", ""))
