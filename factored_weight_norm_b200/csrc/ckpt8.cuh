@@ -244,21 +244,22 @@ __global__ void __launch_bounds__(256, 2) compose_fwd_ckpt8_kernel(
 // ----------------------------------------------------------------- backward
 // compose_bwd_kernel's schedule (compose.cuh) with z read from the codes: a
 // CTA takes one 128-column strip of a chunk of rows, each thread carries its
-// columns' sums in fp32, and the last CTA of a strip adds the chunks in order.
+// columns' sums in fp32, and the last CTA of a strip adds the chunks' sums in
+// order.  The next rows are in flight while these are multiplied and stored.
 constexpr int kCkptBwdThreads = 256;
 constexpr int kCkptBwdRows = 4;  // rows in flight per thread
+constexpr int kCkptMaxChunks = 64;
 
 template <typename L>
 __global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
     const typename L::T* __restrict__ dy, const int8_t* __restrict__ z8, const float* __restrict__ z_scale,
     const float* __restrict__ m, const float* __restrict__ n, float s, long long tokens, long long d_out,
     long long blocks, typename L::T* __restrict__ d_base, typename L::T* __restrict__ d_lora,
-    float* __restrict__ partial, unsigned long long* __restrict__ counters, float* __restrict__ d_m,
-    long long rows_per_chunk, unsigned long long epoch) {
+    float* __restrict__ partial, unsigned long long* __restrict__ marks, float* __restrict__ d_m,
+    long long rows_per_chunk, unsigned long long tag) {
   constexpr int E = L::kE;
   constexpr int kSlots = kCkptBwdThreads / L::kLanes;  // rows visited at once
   __shared__ float red[kSlots][kCkptBlock];
-  __shared__ int is_last;
   const int gl = threadIdx.x % L::kLanes, slot = threadIdx.x / L::kLanes;
   const long long block = blockIdx.x;
   const long long col0 = block * kCkptBlock;
@@ -273,10 +274,10 @@ __global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
   if (L::any(gl, left)) {
     const long long row0 = blockIdx.y * rows_per_chunk;
     const long long row1 = min(tokens, row0 + rows_per_chunk);
-    for (long long row = row0 + slot; row < row1; row += kCkptBwdRows * kSlots) {
-      typename L::Raw ra[kCkptBwdRows];
-      typename L::Codes rz[kCkptBwdRows];
-      float sc[kCkptBwdRows];
+    typename L::Raw ra[kCkptBwdRows];
+    typename L::Codes rz[kCkptBwdRows];
+    float sc[kCkptBwdRows];
+    const auto fetch = [&](long long row) {
 #pragma unroll
       for (int u = 0; u < kCkptBwdRows; ++u) {
         const long long rr = row + u * kSlots;
@@ -286,18 +287,31 @@ __global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
           sc[u] = __ldg(z_scale + rr * blocks + block);
         }
       }
+    };
+    fetch(row0 + slot);
+    for (long long row = row0 + slot; row < row1; row += kCkptBwdRows * kSlots) {
+      typename L::Raw ca[kCkptBwdRows];
+      typename L::Codes cz[kCkptBwdRows];
+      float cs[kCkptBwdRows];
+#pragma unroll
+      for (int u = 0; u < kCkptBwdRows; ++u) {
+        ca[u] = ra[u];
+        cz[u] = rz[u];
+        cs[u] = sc[u];
+      }
+      fetch(row + kCkptBwdRows * kSlots);
 #pragma unroll
       for (int u = 0; u < kCkptBwdRows; ++u) {
         const long long rr = row + u * kSlots;
         if (rr < row1) {
           float a[E], z[E], db[E], dl[E];
-          L::unpack(ra[u], a);
-          L::unpack_code(rz[u], z);
+          L::unpack(ca[u], a);
+          L::unpack_code(cz[u], z);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             db[e] = g[e] * a[e];
             dl[e] = s * db[e];
-            acc[e] = fmaf(a[e], z[e] * sc[u], acc[e]);
+            acc[e] = fmaf(a[e], z[e] * cs[u], acc[e]);
           }
           L::store(d_base + rr * d_out + col0, gl, left, db);
           L::store(d_lora + rr * d_out + col0, gl, left, dl);
@@ -316,32 +330,37 @@ __global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
     for (int w = 0; w < kSlots; ++w) sum += red[w][t];
     partial[blockIdx.y * d_out + col0 + t] = sum;
   }
+  // Each CTA marks its chunk with this call's tag and then looks whether every
+  // chunk of the strip carries it; the one whose mark comes last does (between
+  // a CTA's mark and its look stands a sequentially consistent fence), and any
+  // other that sees all marks writes the same values.  The marks need no
+  // clearing before the launch, whatever the workspace held; they are wiped at
+  // the end, so that a replay of the same launch starts clean.  (A tagged
+  // counter per strip, raised by compare-and-swap, took 12 us of 17 at 512 x
+  // 1024: 32 CTAs arrive at once and retry one after another.)
   __threadfence();
   __syncthreads();
-  // arrivals tagged with this call's epoch, as in compose_bwd_kernel: a word
-  // with another tag counts as zero, so nothing is cleared before the launch
-  const unsigned long long tag = epoch << 8;
-  if (t == 0) {
-    unsigned long long* c = counters + block;
-    unsigned long long v = *reinterpret_cast<volatile unsigned long long*>(c);
-    int seen = 0;
-    while (true) {
-      seen = (v & ~0xffull) == tag ? static_cast<int>(v & 0xffull) : 0;
-      const unsigned long long prev = atomicCAS(c, v, tag | static_cast<unsigned long long>(seen + 1));
-      if (prev == v) break;
-      v = prev;
-    }
-    is_last = (seen == static_cast<int>(gridDim.y) - 1);
-  }
+  unsigned long long* strip_marks = marks + blockIdx.x * static_cast<long long>(kCkptMaxChunks);
+  if (t == 0) *reinterpret_cast<volatile unsigned long long*>(strip_marks + blockIdx.y) = tag;
+  asm volatile("fence.sc.gpu;" ::: "memory");
   __syncthreads();
-  if (is_last) {
+  asm volatile("fence.sc.gpu;" ::: "memory");
+  const bool seen = t >= static_cast<int>(gridDim.y) ||
+                    *reinterpret_cast<volatile unsigned long long*>(strip_marks + t) == tag;
+  if (__syncthreads_and(seen)) {
     __threadfence();
     if (t_ok) {
-      float total = 0.f;
-      for (unsigned c = 0; c < gridDim.y; ++c) total += ld_cg_f32(&partial[c * d_out + col0 + t]);
+      float total = 0.f;  // in chunk order, the loads of 16 chunks at a time
+      for (unsigned k = 0; k < gridDim.y; k += 16) {
+        float p[16];
+#pragma unroll
+        for (unsigned j = 0; j < 16; ++j) p[j] = k + j < gridDim.y ? __ldcg(&partial[(k + j) * d_out + col0 + t]) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) total += p[j];
+      }
       d_m[col0 + t] = total / __ldg(n + col0 + t);
     }
-    if (t == 0) counters[block] = tag;  // count 0 under this tag: a replay of the same launch starts clean
+    if (t < static_cast<int>(gridDim.y)) strip_marks[t] = 0;
   }
 }
 

@@ -1195,16 +1195,17 @@ void launch_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_s
   using T = typename L::T;
   const long long blocks = cdiv(d_out, kCkptBlock);
   const long long slots = static_cast<long long>(dev->num_sms) * ctas_per_sm(compose_bwd_ckpt8_kernel<L>, kCkptBwdThreads);
-  const long long chunks = bwd_chunks(blocks, slots, tokens,
-                                      std::min<long long>(kMaxBwdChunks, cdiv(tokens, kCkptBwdThreads / L::kLanes)));
+  // at least one row for each row of lanes
+  const long long most = cdiv(tokens, kCkptBwdThreads / L::kLanes);
+  const long long chunks = bwd_chunks(blocks, slots, tokens, std::min<long long>(kCkptMaxChunks, most));
   const long long rows = cdiv(tokens, chunks);
-  unsigned long long* cnt = reinterpret_cast<unsigned long long*>(ws);  // tagged: no clearing needed
-  float* part = reinterpret_cast<float*>(ws + align_up(blocks * 8, 256));
+  unsigned long long* marks = reinterpret_cast<unsigned long long*>(ws);  // tagged: no clearing needed
+  float* part = reinterpret_cast<float*>(ws + blocks * kCkptMaxChunks * 8);
   note_launch();
   compose_bwd_ckpt8_kernel<L><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(cdiv(tokens, rows))),
                                 kCkptBwdThreads, 0, st>>>(
       static_cast<const T*>(dy), z8, z_scale, m, n, s, tokens, d_out, blocks, static_cast<T*>(d_base),
-      static_cast<T*>(d_lora), part, cnt, d_m, rows, next_bwd_epoch());
+      static_cast<T*>(d_lora), part, marks, d_m, rows, next_bwd_epoch() + 1);
 }
 
 }  // namespace
@@ -1382,8 +1383,8 @@ int dora_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const voi
 size_t dora_compose_bwd_ckpt8_workspace_size(int64_t tokens, int64_t d_out) {
   if (tokens < 0 || d_out < 0) return 0;
   const int64_t d = std::max<int64_t>(d_out, 1);
-  return align_up(static_cast<size_t>(cdiv(d, kCkptBlock)) * 8, 256) +
-         align_up(static_cast<size_t>(kMaxBwdChunks) * d * 4, 256);
+  return static_cast<size_t>(cdiv(d, kCkptBlock)) * kCkptMaxChunks * 8 +
+         align_up(static_cast<size_t>(kCkptMaxChunks) * d * 4, 256);
 }
 
 int dora_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_scale, const float* m, const float* n,
