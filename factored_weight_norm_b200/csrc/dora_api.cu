@@ -169,7 +169,6 @@ int device_info(DeviceInfo** out) {
     if (pair_attrs(linear_pair_kernel<false, false>, d.smem_optin) ||
         pair_attrs(linear_pair_kernel<false, true>, d.smem_optin) ||
         pair_attrs(linear_pair_kernel<true, true>, d.smem_optin) ||
-        pair_attrs(linear_pair_kernel<false, false, true>, d.smem_optin) ||
         pair_attrs(linear_i8_pair_kernel, d.smem_optin) || pair_attrs(linear_ckpt8_pair_kernel, d.smem_optin))
       return DORA_ERR_CUDA;
     for (int i8 = 0; i8 < 2; ++i8)
@@ -916,11 +915,10 @@ cudaLaunchConfig_t pair_config(cudaLaunchAttribute (&attrs)[2], int threads, siz
   return cfg;
 }
 
-// P = bf16(s * x A^T) into `P` [tokens, r], what the rounding leaves into `P_lo`
-// unless that is null; ordered after everything before it on the stream.  tmA
-// has boxes of pick_bn(r) / 2 rows.
-int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, __nv_bfloat16* P_lo, float s,
-             int64_t tokens, int64_t d_in, int64_t r, const DeviceInfo* dev, cudaStream_t st) {
+// P = bf16(s * x A^T) into `P` [tokens, r]; ordered after everything before it
+// on the stream.  tmA has boxes of pick_bn(r) / 2 rows.
+int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, float s, int64_t tokens, int64_t d_in,
+             int64_t r, const DeviceInfo* dev, cudaStream_t st) {
   LinearArgs pa{};
   pa.M = static_cast<int>(tokens);
   pa.N = static_cast<int>(r);
@@ -931,7 +929,6 @@ int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, _
   pa.stages = linear_pair_stages(dev->smem_optin);
   pa.alpha = s;
   pa.out = P;
-  pa.out_lo = P_lo;
   pa.ldo = r;
   pa.wait_limit = kWaitLimitCycles;
   pa.status = dev->status;
@@ -939,8 +936,7 @@ int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, _
   cudaLaunchConfig_t cfg = pair_config(attrs, kLinThreads, linear_pair_smem(dev->smem_optin),
                                        static_cast<long long>(pa.tiles_m) * pa.tiles_n, false, dev, st);
   note_launch();
-  return cudaLaunchKernelEx(&cfg, P_lo ? linear_pair_kernel<false, false, true> : linear_pair_kernel<false, false>, tmX,
-                            tmA, tmX, tmA, pa) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<false, false>, tmX, tmA, tmX, tmA, pa) == cudaSuccess
              ? DORA_OK
              : DORA_ERR_CUDA;
 }
@@ -980,6 +976,22 @@ int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const 
                                                                                                : DORA_ERR_CUDA;
 }
 
+// P = bf16(s * x A^T), and what the rounding leaves unless P_lo is null, on
+// slices: few rank rows make few large tiles, so K is split instead.
+int launch_p_slice(const void* x, const void* A, __nv_bfloat16* P, __nv_bfloat16* P_lo, float s, int64_t tokens,
+                   int64_t d_in, int64_t r, const DeviceInfo* dev, cudaStream_t st) {
+  CUtensorMap tmX, tmA;
+  if (make_map(&tmA, A, r, d_in) || make_map(&tmX, x, tokens, d_in, slice_bn(tokens))) return DORA_ERR_CUDA;
+  SliceArgs sa{};
+  sa.rows = static_cast<int>(r);
+  sa.tokens = static_cast<int>(tokens);
+  sa.kb_main = sa.kb_total = static_cast<int>(cdiv(d_in, kLinBK));
+  sa.alpha = s;
+  sa.out = P;
+  sa.out_lo = P_lo;
+  return launch_slice(false, tmA, tmX, tmA, tmX, sa, false, dev, st);
+}
+
 int fused_linear(const void* x, const void* W, const void* A, const void* B, const void* bias, const float* m,
                  const float* n, float s, int64_t tokens, int64_t d_in, int64_t d_out, int64_t r, dora_dtype dt,
                  void* y, bool ckpt, int8_t* z8, float* z_scale, void* workspace, size_t workspace_bytes,
@@ -1016,10 +1028,10 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
   const int stages = linear_pair_stages(dev->smem_optin);
   if (stages < 2) return DORA_ERR_UNSUPPORTED;
   const long long tiles_m2 = cdiv(tokens, kPairBM);
-  __nv_bfloat16* P_lo = ckpt && r > 0 ? P + p_bytes / 2 : nullptr;
-  if (r > 0 && launch_p(tmX, tmA, P, P_lo, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
   cudaLaunchAttribute attrs[2];
   if (ckpt) {
+    __nv_bfloat16* P_lo = r > 0 ? P + p_bytes / 2 : nullptr;
+    if (r > 0 && launch_p_slice(x, A, P, P_lo, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
     CUtensorMap tmLo;
     if (r > 0 && make_map(&tmLo, P_lo, tokens, r)) return DORA_ERR_CUDA;
     LinearCkptArgs ca{};
@@ -1047,6 +1059,7 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
     return launch_error();
   }
 
+  if (r > 0 && launch_p(tmX, tmA, P, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
   // 2) y = bf16(g * [x | P] [W | B]^T + b), dependent on 1) only for the extension blocks
   LinearArgs la{};
   la.M = static_cast<int>(tokens);
@@ -1294,22 +1307,15 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
   if (device_info(&dev)) return DORA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* P = static_cast<__nv_bfloat16*>(workspace);
-  CUtensorMap tmXq, tmWq, tmX, tmA, tmP, tmB;
+  CUtensorMap tmXq, tmWq, tmP, tmB;
   if (tokens <= kSliceTokens) {
     const uint32_t bn = slice_bn(tokens);
     if (make_map_i8(&tmWq, W_q, d_out, d_in, kLinBM) || make_map_i8(&tmXq, x_q, tokens, d_in, bn)) return DORA_ERR_CUDA;
     SliceArgs sa{};
     sa.tokens = static_cast<int>(tokens);
-    if (r > 0) {
-      if (make_map(&tmA, A, r, d_in) || make_map(&tmX, x, tokens, d_in, bn) || make_map(&tmB, B, d_out, r) ||
-          make_map(&tmP, P, tokens, r, bn))
-        return DORA_ERR_CUDA;
-      sa.rows = static_cast<int>(r);
-      sa.kb_main = sa.kb_total = static_cast<int>(cdiv(d_in, kLinBK));
-      sa.alpha = s;
-      sa.out = P;
-      if (launch_slice(false, tmA, tmX, tmA, tmX, sa, false, dev, st)) return DORA_ERR_CUDA;
-    }
+    if (r > 0 && (make_map(&tmB, B, d_out, r) || make_map(&tmP, P, tokens, r, bn) ||
+                  launch_p_slice(x, A, P, nullptr, s, tokens, d_in, r, dev, st)))
+      return DORA_ERR_CUDA;
     sa.rows = static_cast<int>(d_out);
     sa.kb_main = static_cast<int>(cdiv(d_in, kI8BK));
     sa.kb_total = sa.kb_main + static_cast<int>(cdiv(r, kLinBK));
@@ -1323,12 +1329,9 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
   }
   if (make_map_i8(&tmXq, x_q, tokens, d_in, kLinBM) || make_map_i8(&tmWq, W_q, d_out, d_in, kPairBN / 2))
     return DORA_ERR_CUDA;
-  if (r > 0) {
-    if (make_map(&tmX, x, tokens, d_in) || make_map(&tmA, A, r, d_in, pick_bn(r) / 2) || make_map(&tmP, P, tokens, r) ||
-        make_map(&tmB, B, d_out, r, kPairBN / 2))
-      return DORA_ERR_CUDA;
-    if (launch_p(tmX, tmA, P, nullptr, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
-  }
+  if (r > 0 && (make_map(&tmP, P, tokens, r) || make_map(&tmB, B, d_out, r, kPairBN / 2) ||
+                launch_p_slice(x, A, P, nullptr, s, tokens, d_in, r, dev, st)))
+    return DORA_ERR_CUDA;
   LinearI8Args la{};
   la.M = static_cast<int>(tokens);
   la.N = static_cast<int>(d_out);

@@ -257,31 +257,71 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       }
       const long long row = static_cast<long long>(tm) * kPairBM + rank * kLinBM + q * 32 + lane;
       const int col0 = tn * kPairBN + half * 128;
-      if (alive && row < a.M && col0 < a.N) {
+      if (alive && col0 < a.N) {  // warp-uniform
         // columns past N are sums of zero-filled operands: they do not count
         const uint32_t top = __float_as_uint(max_abs<128>(0.f, v));
         const float inv = top_inverse(top);
-        a.z_scale[row * blocks + col0 / kCkptBlock] = top_scale(top);
+        if (row < a.M) a.z_scale[row * blocks + col0 / kCkptBlock] = top_scale(top);
         const float* gv = cf + half * 128;
+        const int piece = lane & 3;
+        const long long row4 = row - piece;
+        uint4 zk[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (col0 + j * 8 >= a.N) break;
-          float z[8];
-          uint32_t qc[8];
+        for (int c = 0; c < 4; ++c) {
+          if (col0 + c * 32 >= a.N) {
+            // pieces past N are transposed with the others and not stored
+            zk[(c & 1) * 2] = zk[(c & 1) * 2 + 1] = make_uint4(0u, 0u, 0u, 0u);
+          } else {
+            uint4 pk[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = v[j * 8 + e];
-          codes_of<8>(z, top, inv, qc);
-          CodeIO<8>::store(a.z8 + row * a.N + col0 + j * 8, qc);
+            for (int j = 0; j < 4; ++j) {
+              const int k = c * 32 + j * 8;
+              float z[8];
+              uint32_t qc[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = fmaf(gv[j * 8 + e], z[e], gv[kPairBN + j * 8 + e]);
-          uint4 pk;
-          pk.x = pack_bf16x2(z[0], z[1]);
-          pk.y = pack_bf16x2(z[2], z[3]);
-          pk.z = pack_bf16x2(z[4], z[5]);
-          pk.w = pack_bf16x2(z[6], z[7]);
-          *reinterpret_cast<uint4*>(a.y + row * a.N + col0 + j * 8) = pk;
+              for (int e = 0; e < 8; ++e) z[e] = v[k + e];
+              codes_of<8>(z, top, inv, qc);
+              const uint32_t lo = pack_codes(qc[0], qc[1], qc[2], qc[3]), hi = pack_codes(qc[4], qc[5], qc[6], qc[7]);
+              uint4& zp = zk[(c & 1) * 2 + j / 2];
+              if (j & 1) {
+                zp.z = lo;
+                zp.w = hi;
+              } else {
+                zp.x = lo;
+                zp.y = hi;
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) z[e] = fmaf(gv[k + e], z[e], gv[kPairBN + k + e]);
+              pk[j].x = pack_bf16x2(z[0], z[1]);
+              pk[j].y = pack_bf16x2(z[2], z[3]);
+              pk[j].z = pack_bf16x2(z[4], z[5]);
+              pk[j].w = pack_bf16x2(z[6], z[7]);
+            }
+            __syncwarp();
+            quad_transpose(pk, lane);
+            const int col = col0 + c * 32 + piece * 8;
+            quad_store(reinterpret_cast<uint8_t*>(a.y + row4 * a.N + col), a.N * 2ll, pk, row4, a.M, col < a.N);
+          }
+          if (c & 1) {  // 64 codes a row are whole
+            __syncwarp();
+            quad_transpose(zk, lane);
+            const int col = col0 + (c - 1) * 32 + piece * 16;
+            int8_t* at = a.z8 + row4 * a.N + col;
+            if (a.N % 16 == 0) {
+              quad_store(reinterpret_cast<uint8_t*>(at), a.N, zk, row4, a.M, col < a.N);
+            } else {  // rows start on 8 bytes, and the last piece may be half a one
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (row4 + j < a.M) {
+                  if (col < a.N) *reinterpret_cast<uint2*>(at + static_cast<long long>(j) * a.N) = make_uint2(zk[j].x, zk[j].y);
+                  if (col + 8 < a.N)
+                    *reinterpret_cast<uint2*>(at + static_cast<long long>(j) * a.N + 8) = make_uint2(zk[j].z, zk[j].w);
+                }
+            }
+          }
         }
       }
+      __syncwarp();
     }
   }
 

@@ -45,6 +45,41 @@ __device__ __forceinline__ void epi_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kI8EpiThreads) : "memory");
 }
 
+// Transposes the 16-byte pieces of four neighbouring lanes: lane i of a quad
+// ends with every lane's piece i, c[j] being lane j's.  A thread of the epilogue
+// has a row of its tile; stored as it is, each store touches 32 rows, 16 bytes
+// of each, and takes the memory pipeline 32 passes.  Transposed, a store
+// touches 64 bytes of 8 rows.
+__device__ __forceinline__ void quad_transpose(uint4 (&c)[4], int lane) {
+  const auto swap = [&](uint4& lo, uint4& hi, bool upper, int o) {
+    // the upper lane of the two gives its lo for the lower one's hi
+    const uint4 give = upper ? lo : hi;
+    uint4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, o);
+    got.y = __shfl_xor_sync(0xffffffffu, give.y, o);
+    got.z = __shfl_xor_sync(0xffffffffu, give.z, o);
+    got.w = __shfl_xor_sync(0xffffffffu, give.w, o);
+    if (upper)
+      lo = got;
+    else
+      hi = got;
+  };
+  swap(c[0], c[1], lane & 1, 1);
+  swap(c[2], c[3], lane & 1, 1);
+  swap(c[0], c[2], lane & 2, 2);
+  swap(c[1], c[3], lane & 2, 2);
+}
+
+// Stores the transposed pieces of a quad: lane i has piece i (16 bytes, 64 of
+// them a row) of rows row4 .. row4 + 3; `at` is the address of its piece in
+// row4, rows are `pitch` bytes apart.
+__device__ __forceinline__ void quad_store(uint8_t* at, long long pitch, const uint4 (&c)[4], long long row4,
+                                           int rows, bool col_ok) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (col_ok && row4 + j < rows) *reinterpret_cast<uint4*>(at + j * pitch) = c[j];
+}
+
 // The pair GEMM of linear_tc.cuh (256 x 256 tiles, two K blocks per stage, the
 // same barriers and ring) with the int8 base in TMEM columns 0..255 and the
 // adapter in 256..511.  One tile's two accumulators fill the TMEM, so the next
@@ -275,6 +310,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       if (lane == 0) mbar_arrive_cluster(base_empty_leader);
       const int col0 = tn * kPairBN + half * 128;
       const float* swg = cf + half * 128;
+      const int piece = lane & 3;
+      const long long row4 = row - piece;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         float u[32];
@@ -286,9 +323,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             if (lane == 0) mbar_arrive_cluster(ext_empty_leader);
           }
         }
+        if (col0 + c * 32 >= a.N) continue;  // warp-uniform
+        uint4 pk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (col0 + c * 32 + j * 8 >= a.N) continue;  // warp-uniform
           float o[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -296,15 +334,15 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             const float b = has_ext ? fmaf(swg[kPairBN + k], u[j * 8 + e], swg[2 * kPairBN + k]) : swg[2 * kPairBN + k];
             o[e] = fmaf(v[k], swg[k], b);
           }
-          if (row_ok) {
-            uint4 pk;
-            pk.x = pack_bf16x2(o[0], o[1]);
-            pk.y = pack_bf16x2(o[2], o[3]);
-            pk.z = pack_bf16x2(o[4], o[5]);
-            pk.w = pack_bf16x2(o[6], o[7]);
-            *reinterpret_cast<uint4*>(a.y + row * a.N + col0 + c * 32 + j * 8) = pk;
-          }
+          pk[j].x = pack_bf16x2(o[0], o[1]);
+          pk[j].y = pack_bf16x2(o[2], o[3]);
+          pk[j].z = pack_bf16x2(o[4], o[5]);
+          pk[j].w = pack_bf16x2(o[6], o[7]);
         }
+        quad_transpose(pk, lane);
+        const int col = col0 + c * 32 + piece * 8;
+        quad_store(reinterpret_cast<uint8_t*>(a.y + row4 * a.N + col), a.N * 2ll, pk, row4, a.M, col < a.N);
+        __syncwarp();
       }
     }
   }

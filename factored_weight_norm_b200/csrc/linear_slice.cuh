@@ -41,6 +41,7 @@ struct SliceArgs {
   const __nv_bfloat16* bias;
   float alpha;            // !I8: scale of the product
   __nv_bfloat16* out;     // [tokens, rows]
+  __nv_bfloat16* out_lo;  // !I8: what the output's rounding leaves, or null
   long long wait_limit;
   int* status;
 };
@@ -284,7 +285,16 @@ __global__ void __launch_bounds__(kSlThreads)
         pk.y = pack_bf16x2(o[2], o[3]);
         pk.z = pack_bf16x2(o[4], o[5]);
         pk.w = pack_bf16x2(o[6], o[7]);
-        *reinterpret_cast<uint4*>(a.out + static_cast<long long>(t) * a.rows + row0 + group) = pk;
+        const long long off = static_cast<long long>(t) * a.rows + row0 + group;
+        *reinterpret_cast<uint4*>(a.out + off) = pk;
+        if (!I8 && a.out_lo) {
+          uint4 lo;
+          lo.x = pack_bf16x2(o[0] - bf16_lo(pk.x), o[1] - bf16_hi(pk.x));
+          lo.y = pack_bf16x2(o[2] - bf16_lo(pk.y), o[3] - bf16_hi(pk.y));
+          lo.z = pack_bf16x2(o[4] - bf16_lo(pk.z), o[5] - bf16_hi(pk.z));
+          lo.w = pack_bf16x2(o[6] - bf16_lo(pk.w), o[7] - bf16_hi(pk.w));
+          *reinterpret_cast<uint4*>(a.out_lo + off) = lo;
+        }
       }
     }
     __syncwarp();

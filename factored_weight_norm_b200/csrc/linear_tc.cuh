@@ -62,7 +62,6 @@ struct LinearArgs {
   const __nv_bfloat16* bias;  // per-column bias, or null
   void* out;               // [M, ldo] row-major, bf16 or fp32 (kernel template)
   long long ldo;
-  __nv_bfloat16* out_lo;   // SPLIT: the rest of a bf16 output, [M, ldo]
   int ext_waits;           // 1: the extension operands come from the preceding grid
   long long wait_limit;
   int* status;
@@ -106,9 +105,7 @@ constexpr uint32_t kPairStageBytes = 2 * kPairKps * kLinABytes;
 // B_MN: the B-side operand is stored N-contiguous (its rows run along K), as
 // W is for a contraction over d_out; it is loaded as two 64-column boxes per
 // K block and read through MN-major descriptors.  OUT_F32: fp32 output.
-// SPLIT: what the bf16 output's rounding leaves is written to out_lo, in bf16
-// too, so that the two together hold 16 bits of each value.
-template <bool B_MN, bool OUT_F32, bool SPLIT = false>
+template <bool B_MN, bool OUT_F32>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
                        const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2,
@@ -341,14 +338,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 pk.z = pack_bf16x2(v[8 * j + 4], v[8 * j + 5]);
                 pk.w = pack_bf16x2(v[8 * j + 6], v[8 * j + 7]);
                 *reinterpret_cast<uint4*>(dst_row + col0 + 8 * j) = pk;
-                if (SPLIT) {
-                  uint4 lo;
-                  lo.x = pack_bf16x2(v[8 * j + 0] - bf16_lo(pk.x), v[8 * j + 1] - bf16_hi(pk.x));
-                  lo.y = pack_bf16x2(v[8 * j + 2] - bf16_lo(pk.y), v[8 * j + 3] - bf16_hi(pk.y));
-                  lo.z = pack_bf16x2(v[8 * j + 4] - bf16_lo(pk.z), v[8 * j + 5] - bf16_hi(pk.z));
-                  lo.w = pack_bf16x2(v[8 * j + 6] - bf16_lo(pk.w), v[8 * j + 7] - bf16_hi(pk.w));
-                  *reinterpret_cast<uint4*>(a.out_lo + row * a.ldo + col0 + 8 * j) = lo;
-                }
               }
             }
           }
