@@ -102,114 +102,118 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    int stage = 0;
-    uint32_t phase = 0;
-    uint32_t parity_bits = 0;
-    uint32_t filled_mask = 0;
-    bool ext_ready = a.kb_r == 0;
-    bool ok = true;
-    for (int t = cid; t < n_tiles && ok; t += n_pairs) {
-      int tm, tn;
-      lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
-      const int yx = tm * kPairBM + static_cast<int>(rank) * kLinBM;
-      const int yw = tn * kPairBN + static_cast<int>(rank) * (kPairBN / 2);
-      for (int kb0 = 0; kb0 < kb_total; kb0 += kPairKps) {
-        if (kb0 + kPairKps > a.kb_main && !ext_ready) {
-          grid_dep_wait();  // P comes from the launch before
-          fence_proxy_async_all();
-          ext_ready = true;
-        }
-        bool got = true;
-        if (lane == 0) {
-          got = mbar_wait(&empty[stage], phase ^ 1u, limit);
-          if (got && leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
-          if (!got) lin_timeout(a.status, abort_flag);
-        }
-        got = __shfl_sync(0xffffffffu, got, 0);
-        __syncwarp();
-        if (!got) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = base_s + stage * kPairStageBytes;
-        const uint32_t bar = full_leader + static_cast<uint32_t>(stage) * 8u;
-        if (lane < 2 * kPairKps) {
-          const bool w_side = lane >= kPairKps;
-          const int kb = kb0 + (w_side ? lane - kPairKps : lane);
-          // K blocks past kb_total lie wholly outside the tensor: zero-filled
-          const bool ext = a.kb_r > 0 && kb >= a.kb_main;
-          const bool lo = ext && kb >= a.kb_main + a.kb_r;
-          const int xk = (kb - (ext ? a.kb_main : 0) - (lo ? a.kb_r : 0)) * kLinBK;
-          const CUtensorMap* map = w_side ? (ext ? &tmB : &tmW) : (lo ? &tmLo : (ext ? &tmHi : &tmX));
-          tma_load_2d_pair(dst + lane * kLinABytes, map, bar, xk, w_side ? yw : yx);
-        }
-        parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
-        filled_mask |= 1u << stage;
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    // never leave a TMA copy in flight: the even CTA's full barriers count both CTAs' bytes
-    if (lane == 0 && leader)
-      for (int s2 = 0; s2 < a.stages; ++s2)
-        if ((filled_mask >> s2) & 1u) mbar_wait(&full[s2], (parity_bits >> s2) & 1u, limit);
-  } else if (warp == 1) {
-    // ------------------------------------------- MMA issuer (even CTA only)
-    if (leader && lane == 0) {
+  if (warp < 4) {
+    regs_give<kI8RegsFew>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
       int stage = 0;
       uint32_t phase = 0;
+      uint32_t parity_bits = 0;
+      uint32_t filled_mask = 0;
+      bool ext_ready = a.kb_r == 0;
       bool ok = true;
-      const uint32_t idesc = idesc_bf16_f32(kPairBM, kPairBN);
-      const uint64_t desc0 = sw128_kmajor_desc(base_s);
-      const uint64_t desc_step = kPairStageBytes >> 4;
-      uint32_t it = 0;  // chunks so far
       for (int t = cid; t < n_tiles && ok; t += n_pairs) {
-        for (int c = 0; c < n_chunks && ok; ++c, ++it) {
-          const uint32_t ab = it & 1u;
-          if (!mbar_wait(&acc_empty[ab], ((it >> 1) & 1u) ^ 1u, limit)) {
-            lin_timeout(a.status, abort_flag);
+        int tm, tn;
+        lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
+        const int yx = tm * kPairBM + static_cast<int>(rank) * kLinBM;
+        const int yw = tn * kPairBN + static_cast<int>(rank) * (kPairBN / 2);
+        for (int kb0 = 0; kb0 < kb_total; kb0 += kPairKps) {
+          if (kb0 + kPairKps > a.kb_main && !ext_ready) {
+            grid_dep_wait();  // P comes from the launch before
+            fence_proxy_async_all();
+            ext_ready = true;
+          }
+          bool got = true;
+          if (lane == 0) {
+            got = mbar_wait(&empty[stage], phase ^ 1u, limit);
+            if (got && leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
+            if (!got) lin_timeout(a.status, abort_flag);
+          }
+          got = __shfl_sync(0xffffffffu, got, 0);
+          __syncwarp();
+          if (!got) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t d = tmem + ab * kPairBN;
-          const int s0 = n_stages * c / n_chunks, s1 = n_stages * (c + 1) / n_chunks;
-          for (int s = s0; s < s1; ++s) {
-            if (!mbar_wait(&full[stage], phase, limit)) {
+          const uint32_t dst = base_s + stage * kPairStageBytes;
+          const uint32_t bar = full_leader + static_cast<uint32_t>(stage) * 8u;
+          if (lane < 2 * kPairKps) {
+            const bool w_side = lane >= kPairKps;
+            const int kb = kb0 + (w_side ? lane - kPairKps : lane);
+            // K blocks past kb_total lie wholly outside the tensor: zero-filled
+            const bool ext = a.kb_r > 0 && kb >= a.kb_main;
+            const bool lo = ext && kb >= a.kb_main + a.kb_r;
+            const int xk = (kb - (ext ? a.kb_main : 0) - (lo ? a.kb_r : 0)) * kLinBK;
+            const CUtensorMap* map = w_side ? (ext ? &tmB : &tmW) : (lo ? &tmLo : (ext ? &tmHi : &tmX));
+            tma_load_2d_pair(dst + lane * kLinABytes, map, bar, xk, w_side ? yw : yx);
+          }
+          parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+          filled_mask |= 1u << stage;
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // never leave a TMA copy in flight: the even CTA's full barriers count both CTAs' bytes
+      if (lane == 0 && leader)
+        for (int s2 = 0; s2 < a.stages; ++s2)
+          if ((filled_mask >> s2) & 1u) mbar_wait(&full[s2], (parity_bits >> s2) & 1u, limit);
+    } else if (warp == 1) {
+      // ------------------------------------------- MMA issuer (even CTA only)
+      if (leader && lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t idesc = idesc_bf16_f32(kPairBM, kPairBN);
+        const uint64_t desc0 = sw128_kmajor_desc(base_s);
+        const uint64_t desc_step = kPairStageBytes >> 4;
+        uint32_t it = 0;  // chunks so far
+        for (int t = cid; t < n_tiles && ok; t += n_pairs) {
+          for (int c = 0; c < n_chunks && ok; ++c, ++it) {
+            const uint32_t ab = it & 1u;
+            if (!mbar_wait(&acc_empty[ab], ((it >> 1) & 1u) ^ 1u, limit)) {
               lin_timeout(a.status, abort_flag);
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t adesc = desc0 + static_cast<uint64_t>(stage) * desc_step;
-            const uint64_t bdesc = adesc + ((kPairKps * kLinABytes) >> 4);
+            const uint32_t d = tmem + ab * kPairBN;
+            const int s0 = n_stages * c / n_chunks, s1 = n_stages * (c + 1) / n_chunks;
+            for (int s = s0; s < s1; ++s) {
+              if (!mbar_wait(&full[stage], phase, limit)) {
+                lin_timeout(a.status, abort_flag);
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint64_t adesc = desc0 + static_cast<uint64_t>(stage) * desc_step;
+              const uint64_t bdesc = adesc + ((kPairKps * kLinABytes) >> 4);
 #pragma unroll
-            for (int i = 0; i < kPairKps; ++i)
+              for (int i = 0; i < kPairKps; ++i)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16_pair(d, adesc + i * (kLinABytes >> 4) + 2 * k, bdesc + i * (kLinABytes >> 4) + 2 * k, idesc,
-                              (s > s0 || i > 0 || k > 0) ? 1u : 0u);
-            mma_commit_pair(&empty[stage], 0x3);
-            if (++stage == a.stages) {
-              stage = 0;
-              phase ^= 1u;
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16_pair(d, adesc + i * (kLinABytes >> 4) + 2 * k, bdesc + i * (kLinABytes >> 4) + 2 * k, idesc,
+                                (s > s0 || i > 0 || k > 0) ? 1u : 0u);
+              mma_commit_pair(&empty[stage], 0x3);
+              if (++stage == a.stages) {
+                stage = 0;
+                phase ^= 1u;
+              }
             }
+            if (ok) mma_commit_pair(&acc_full[ab], 0x3);
           }
-          if (ok) mma_commit_pair(&acc_full[ab], 0x3);
         }
+        mma_commit_pair(drain, 0x1);
+        mbar_wait(drain, 0, limit);
       }
-      mma_commit_pair(drain, 0x1);
-      mbar_wait(drain, 0, limit);
     }
   } else {
+    regs_take<kI8RegsMany>();
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    const int half = (warp - 2) >> 2;  // columns half * 128 .. of the tile
-    const int et = threadIdx.x - 64;
+    const int half = (warp - 4) >> 2;  // columns half * 128 .. of the tile
+    const int et = threadIdx.x - 128;
     const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
     const int blocks = (a.N + kCkptBlock - 1) / kCkptBlock;
@@ -290,8 +294,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 zp.x = lo;
                 zp.y = hi;
               }
+              float g[8], b[8];
+              ld_shared8(gv + k, g);
+              ld_shared8(gv + kPairBN + k, b);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) z[e] = fmaf(gv[k + e], z[e], gv[kPairBN + k + e]);
+              for (int e = 0; e < 8; ++e) z[e] = fmaf(g[e], z[e], b[e]);
               pk[j].x = pack_bf16x2(z[0], z[1]);
               pk[j].y = pack_bf16x2(z[2], z[3]);
               pk[j].z = pack_bf16x2(z[4], z[5]);

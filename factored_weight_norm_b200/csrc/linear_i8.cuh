@@ -14,7 +14,13 @@
 
 namespace dora {
 
-constexpr int kI8Threads = 320;  // producer, MMA issuer, eight epilogue warps
+// Three warpgroups: producer and MMA issuer (two warps idle), two of epilogue
+// warps.  The epilogue holds 128 accumulators a thread beside its factors and
+// outputs, so the first warpgroup gives it registers: 384 threads are launched
+// with 168 each, and 128 * 40 + 256 * 232 = 384 * 168.
+constexpr int kI8Threads = 384;
+constexpr int kI8RegsFew = 40, kI8RegsMany = 232;
+static_assert(128 * kI8RegsFew + 256 * kI8RegsMany <= kI8Threads * 168, "register shares");
 constexpr int kI8BK = 128;       // int8 K block: 128 bytes, as 64 bf16 are
 constexpr int64_t kI8MaxDIn = 131056;  // the largest multiple of 16 with 2^14 * d_in < 2^31
 constexpr int kI8EpiThreads = 256;
@@ -38,6 +44,13 @@ struct LinearI8Args {
   long long wait_limit;
   int* status;
 };
+
+// Eight neighbouring floats of shared memory (16-byte aligned).
+__device__ __forceinline__ void ld_shared8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
 
 // Synchronises the eight epilogue warps.
 __device__ __forceinline__ void epi_sync() {
@@ -145,125 +158,129 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    int stage = 0;
-    uint32_t phase = 0;
-    uint32_t parity_bits = 0;
-    uint32_t filled_mask = 0;
-    bool ext_ready = !has_ext;
-    bool ok = true;
-    for (int t = cid; t < n_tiles && ok; t += n_pairs) {
-      int tm, tn;
-      lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
-      const int yx = tm * kPairBM + static_cast<int>(rank) * kLinBM;
-      const int yw = tn * kPairBN + static_cast<int>(rank) * (kPairBN / 2);
-      for (int kb0 = 0; kb0 < a.kb_total; kb0 += kPairKps) {
-        if (kb0 + kPairKps > a.kb_main && !ext_ready) {
-          grid_dep_wait();  // P comes from the launch before
-          fence_proxy_async_all();
-          ext_ready = true;
-        }
-        bool got = true;
-        if (lane == 0) {
-          got = mbar_wait(&empty[stage], phase ^ 1u, limit);
-          if (got && leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
-          if (!got) lin_timeout(a.status, abort_flag);
-        }
-        got = __shfl_sync(0xffffffffu, got, 0);
-        __syncwarp();
-        if (!got) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = base_s + stage * kPairStageBytes;
-        const uint32_t bar = full_leader + static_cast<uint32_t>(stage) * 8u;
-        if (lane < 2 * kPairKps) {
-          const bool w_side = lane >= kPairKps;
-          const int kb = kb0 + (w_side ? lane - kPairKps : lane);
-          // K blocks past kb_total lie wholly outside the tensor: zero-filled
-          const bool ext = has_ext && kb >= a.kb_main;
-          const int xk = ext ? (kb - a.kb_main) * kLinBK : kb * kI8BK;
-          const CUtensorMap* map = w_side ? (ext ? &tmB : &tmW) : (ext ? &tmP : &tmX);
-          tma_load_2d_pair(dst + lane * kLinABytes, map, bar, xk, w_side ? yw : yx);
-        }
-        parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
-        filled_mask |= 1u << stage;
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    // never leave a TMA copy in flight: the even CTA's full barriers count both CTAs' bytes
-    if (lane == 0 && leader)
-      for (int s2 = 0; s2 < a.stages; ++s2)
-        if ((filled_mask >> s2) & 1u) mbar_wait(&full[s2], (parity_bits >> s2) & 1u, limit);
-  } else if (warp == 1) {
-    // ------------------------------------------- MMA issuer (even CTA only)
-    if (leader && lane == 0) {
+  if (warp < 4) {
+    regs_give<kI8RegsFew>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
       int stage = 0;
       uint32_t phase = 0;
+      uint32_t parity_bits = 0;
+      uint32_t filled_mask = 0;
+      bool ext_ready = !has_ext;
       bool ok = true;
-      const uint32_t idesc_b = idesc_i8_s32(kPairBM, kPairBN);
-      const uint32_t idesc_e = idesc_bf16_f32(kPairBM, kPairBN);
-      const uint64_t desc0 = sw128_kmajor_desc(base_s);
-      const uint64_t desc_step = kPairStageBytes >> 4;
-      uint32_t it = 0;
-      for (int t = cid; t < n_tiles && ok; t += n_pairs, ++it) {
-        if (!mbar_wait(base_empty, (it & 1u) ^ 1u, limit)) {
-          lin_timeout(a.status, abort_flag);
-          break;
-        }
-        tc_fence_after();
-        bool ext_free = false;
+      for (int t = cid; t < n_tiles && ok; t += n_pairs) {
+        int tm, tn;
+        lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
+        const int yx = tm * kPairBM + static_cast<int>(rank) * kLinBM;
+        const int yw = tn * kPairBN + static_cast<int>(rank) * (kPairBN / 2);
         for (int kb0 = 0; kb0 < a.kb_total; kb0 += kPairKps) {
-          if (!mbar_wait(&full[stage], phase, limit)) {
-            lin_timeout(a.status, abort_flag);
+          if (kb0 + kPairKps > a.kb_main && !ext_ready) {
+            grid_dep_wait();  // P comes from the launch before
+            fence_proxy_async_all();
+            ext_ready = true;
+          }
+          bool got = true;
+          if (lane == 0) {
+            got = mbar_wait(&empty[stage], phase ^ 1u, limit);
+            if (got && leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
+            if (!got) lin_timeout(a.status, abort_flag);
+          }
+          got = __shfl_sync(0xffffffffu, got, 0);
+          __syncwarp();
+          if (!got) {
             ok = false;
             break;
           }
-          if (has_ext && !ext_free && kb0 + kPairKps > a.kb_main) {
-            if (!mbar_wait(ext_empty, (it & 1u) ^ 1u, limit)) {
-              lin_timeout(a.status, abort_flag);
-              ok = false;
-              break;
-            }
-            ext_free = true;
+          const uint32_t dst = base_s + stage * kPairStageBytes;
+          const uint32_t bar = full_leader + static_cast<uint32_t>(stage) * 8u;
+          if (lane < 2 * kPairKps) {
+            const bool w_side = lane >= kPairKps;
+            const int kb = kb0 + (w_side ? lane - kPairKps : lane);
+            // K blocks past kb_total lie wholly outside the tensor: zero-filled
+            const bool ext = has_ext && kb >= a.kb_main;
+            const int xk = ext ? (kb - a.kb_main) * kLinBK : kb * kI8BK;
+            const CUtensorMap* map = w_side ? (ext ? &tmB : &tmW) : (ext ? &tmP : &tmX);
+            tma_load_2d_pair(dst + lane * kLinABytes, map, bar, xk, w_side ? yw : yx);
           }
-          tc_fence_after();
-          const uint64_t adesc = desc0 + static_cast<uint64_t>(stage) * desc_step;
-          const uint64_t bdesc = adesc + ((kPairKps * kLinABytes) >> 4);
-#pragma unroll
-          for (int i = 0; i < kPairKps; ++i) {
-            const int kb = kb0 + i;
-            const uint64_t ad = adesc + i * (kLinABytes >> 4), bd = bdesc + i * (kLinABytes >> 4);
-            if (has_ext && kb >= a.kb_main) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16_pair(tmem + kPairBN, ad + 2 * k, bd + 2 * k, idesc_e, (kb > a.kb_main || k > 0) ? 1u : 0u);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_i8_pair(tmem, ad + 2 * k, bd + 2 * k, idesc_b, (kb > 0 || k > 0) ? 1u : 0u);
-            }
-          }
-          mma_commit_pair(&empty[stage], 0x3);
+          parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+          filled_mask |= 1u << stage;
           if (++stage == a.stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok) mma_commit_pair(acc_full, 0x3);
       }
-      mma_commit_pair(drain, 0x1);
-      mbar_wait(drain, 0, limit);
+      // never leave a TMA copy in flight: the even CTA's full barriers count both CTAs' bytes
+      if (lane == 0 && leader)
+        for (int s2 = 0; s2 < a.stages; ++s2)
+          if ((filled_mask >> s2) & 1u) mbar_wait(&full[s2], (parity_bits >> s2) & 1u, limit);
+    } else if (warp == 1) {
+      // ------------------------------------------- MMA issuer (even CTA only)
+      if (leader && lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t idesc_b = idesc_i8_s32(kPairBM, kPairBN);
+        const uint32_t idesc_e = idesc_bf16_f32(kPairBM, kPairBN);
+        const uint64_t desc0 = sw128_kmajor_desc(base_s);
+        const uint64_t desc_step = kPairStageBytes >> 4;
+        uint32_t it = 0;
+        for (int t = cid; t < n_tiles && ok; t += n_pairs, ++it) {
+          if (!mbar_wait(base_empty, (it & 1u) ^ 1u, limit)) {
+            lin_timeout(a.status, abort_flag);
+            break;
+          }
+          tc_fence_after();
+          bool ext_free = false;
+          for (int kb0 = 0; kb0 < a.kb_total; kb0 += kPairKps) {
+            if (!mbar_wait(&full[stage], phase, limit)) {
+              lin_timeout(a.status, abort_flag);
+              ok = false;
+              break;
+            }
+            if (has_ext && !ext_free && kb0 + kPairKps > a.kb_main) {
+              if (!mbar_wait(ext_empty, (it & 1u) ^ 1u, limit)) {
+                lin_timeout(a.status, abort_flag);
+                ok = false;
+                break;
+              }
+              ext_free = true;
+            }
+            tc_fence_after();
+            const uint64_t adesc = desc0 + static_cast<uint64_t>(stage) * desc_step;
+            const uint64_t bdesc = adesc + ((kPairKps * kLinABytes) >> 4);
+#pragma unroll
+            for (int i = 0; i < kPairKps; ++i) {
+              const int kb = kb0 + i;
+              const uint64_t ad = adesc + i * (kLinABytes >> 4), bd = bdesc + i * (kLinABytes >> 4);
+              if (has_ext && kb >= a.kb_main) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16_pair(tmem + kPairBN, ad + 2 * k, bd + 2 * k, idesc_e, (kb > a.kb_main || k > 0) ? 1u : 0u);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_i8_pair(tmem, ad + 2 * k, bd + 2 * k, idesc_b, (kb > 0 || k > 0) ? 1u : 0u);
+              }
+            }
+            mma_commit_pair(&empty[stage], 0x3);
+            if (++stage == a.stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (ok) mma_commit_pair(acc_full, 0x3);
+        }
+        mma_commit_pair(drain, 0x1);
+        mbar_wait(drain, 0, limit);
+      }
     }
   } else {
+    regs_take<kI8RegsMany>();
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    const int half = (warp - 2) >> 2;  // columns half * 128 .. of the tile
-    const int et = threadIdx.x - 64;
+    const int half = (warp - 4) >> 2;  // columns half * 128 .. of the tile
+    const int et = threadIdx.x - 128;
     const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     const uint32_t base_empty_leader = mapa_shared(smem_u32(base_empty), 0);
     const uint32_t ext_empty_leader = mapa_shared(smem_u32(ext_empty), 0);
@@ -297,14 +314,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       }
       if (!alive) continue;
       tc_fence_after();
-      float v[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float u[32];
-        tmem_ld32(tmem_lane + c * 32, u);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[c * 32 + e] = static_cast<float>(__float_as_int(u[e])) * sx;
-      }
+      uint32_t acc[128];
+      tmem_ld128(tmem_lane, acc);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(base_empty_leader);
@@ -327,13 +338,17 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         uint4 pk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float o[8];
+          float sw[8], g[8], o[8];
+          const int k = c * 32 + j * 8;
+          ld_shared8(swg + k, sw);
+          ld_shared8(swg + 2 * kPairBN + k, o);
+          if (has_ext) {
+            ld_shared8(swg + kPairBN + k, g);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = c * 32 + j * 8 + e;
-            const float b = has_ext ? fmaf(swg[kPairBN + k], u[j * 8 + e], swg[2 * kPairBN + k]) : swg[2 * kPairBN + k];
-            o[e] = fmaf(v[k], swg[k], b);
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(g[e], u[j * 8 + e], o[e]);
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(static_cast<float>(static_cast<int>(acc[k + e])) * sx, sw[e], o[e]);
           pk[j].x = pack_bf16x2(o[0], o[1]);
           pk[j].y = pack_bf16x2(o[2], o[3]);
           pk[j].z = pack_bf16x2(o[4], o[5]);
