@@ -174,7 +174,7 @@ int device_info(DeviceInfo** out) {
     for (int i8 = 0; i8 < 2; ++i8)
       for (int bn : {16, 32, 64, 128})
         if (cudaFuncSetAttribute(slice_kernel(i8 != 0, bn), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kSlSmem)) != cudaSuccess ||
+                                 static_cast<int>(slice_smem(i8 != 0, bn))) != cudaSuccess ||
             cudaFuncSetAttribute(slice_kernel(i8 != 0, bn), cudaFuncAttributePreferredSharedMemoryCarveout,
                                  cudaSharedmemCarveoutMaxShared) != cudaSuccess)
           return DORA_ERR_CUDA;
@@ -948,13 +948,14 @@ constexpr int64_t kSliceTokens = 128;
 int slice_bn(int64_t tokens) { return tokens <= 16 ? 16 : (tokens <= 32 ? 32 : (tokens <= 64 ? 64 : 128)); }
 
 // One slice launch over `a`: K split over as many CTAs of a cluster as keep
-// the grid within two CTAs an SM.
+// the grid within what is resident at once.
 int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const CUtensorMap& tmB,
                  const CUtensorMap& tmP, SliceArgs a, bool after, const DeviceInfo* dev, cudaStream_t st) {
   const int bn = slice_bn(a.tokens);
   const long long row_tiles = cdiv(a.rows, kLinBM), tok_tiles = cdiv(a.tokens, bn);
+  const long long most = static_cast<long long>(slice_ctas(i8, bn)) * dev->num_sms;
   int splits = 1;
-  while (splits < 8 && 2 * splits <= a.kb_main && row_tiles * tok_tiles * splits <= dev->num_sms) splits *= 2;
+  while (splits < 8 && 2 * splits <= a.kb_main && 2 * row_tiles * tok_tiles * splits <= most) splits *= 2;
   a.wait_limit = kWaitLimitCycles;
   a.status = dev->status;
   cudaLaunchAttribute attrs[2];
@@ -969,7 +970,7 @@ int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const 
   cfg.attrs = attrs;
   cfg.numAttrs = after ? 2 : 1;
   cfg.blockDim = dim3(kSlThreads);
-  cfg.dynamicSmemBytes = kSlSmem;
+  cfg.dynamicSmemBytes = slice_smem(i8, bn);
   cfg.gridDim = dim3(static_cast<unsigned>(row_tiles * splits), static_cast<unsigned>(tok_tiles));
   note_launch();
   return cudaLaunchKernelEx(&cfg, slice_kernel(i8, bn), tmW, tmX, tmB, tmP, a) == cudaSuccess ? DORA_OK

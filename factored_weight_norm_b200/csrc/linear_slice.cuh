@@ -12,6 +12,10 @@
 // tokens from all of them.  int32 partial sums are exact in any order; the
 // adapter's product lies wholly in the last split, so its fp32 sum is one
 // CTA's; the fp32 sums of the down projection are added in split order.
+// The meeting is what costs beyond the stream: it is done once for the whole
+// tile, by all warps, with the loads from all splits in flight together (in
+// two rounds of 64 tokens by four warps, split after split, 128 tokens took 10
+// of 25 us).
 #pragma once
 
 #include "linear_i8.cuh"
@@ -19,14 +23,20 @@
 namespace dora {
 
 constexpr int kSlThreads = 192;  // producer, MMA issuer, four epilogue warps
-constexpr int kSlChunk = 64;     // tokens exchanged at a time
 constexpr int kSlMaxStages = 8;
-constexpr size_t kSlSmem = 112 * 1024;  // two CTAs on an SM
-constexpr size_t kSlFixed = 1024 + 256; // alignment, barriers
+// alignment; row factors (sw * g, g, b) and token scales; barriers
+constexpr size_t kSlFixed = 1024 + (3 * kLinBM + 128) * 4 + 256;
 
+// CTAs an SM and their shared memory: two, but one for the product of 128
+// tokens, whose exchange (int32 sums and the adapter's fp32 beside them) takes
+// 128 KB.
+__host__ __device__ constexpr int slice_ctas(bool i8, int bn) { return i8 && bn > 64 ? 1 : 2; }
+__host__ __device__ constexpr size_t slice_smem(bool i8, int bn) {
+  return slice_ctas(i8, bn) == 2 ? 112 * 1024 : 200 * 1024;
+}
 __host__ __device__ constexpr uint32_t slice_stage_bytes(int bn) { return kLinABytes + bn * 128u; }
-__host__ __device__ constexpr int slice_stages(int bn) {
-  const int n = static_cast<int>((kSlSmem - kSlFixed) / slice_stage_bytes(bn));
+__host__ __device__ constexpr int slice_stages(bool i8, int bn) {
+  const int n = static_cast<int>((slice_smem(i8, bn) - kSlFixed) / slice_stage_bytes(bn));
   return n < kSlMaxStages ? n : kSlMaxStages;
 }
 
@@ -73,6 +83,86 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t
       : "memory");
 }
 
+// One thread's share of the joined tile: eight rows (from `group`) of every
+// token j with j % S == rank that falls to it, from the S splits' exchange
+// areas ([token][128 rows] words; the adapter's behind them in the last one).
+template <bool I8, int BN, int S>
+__device__ __forceinline__ void slice_join(const SliceArgs& a, uint32_t area, const float* rowf, const float* sxs,
+                                           uint32_t rank, int row0, int tok0, bool ext_any) {
+  const int group = (threadIdx.x & 15) * 8;
+  if (row0 + group >= a.rows) return;
+  float swg[8], g[8], b[8];
+  if (I8) {
+    ld_shared8(rowf + group, swg);
+    ld_shared8(rowf + kLinBM + group, g);
+    ld_shared8(rowf + 2 * kLinBM + group, b);
+  }
+#pragma unroll 1
+  for (int j = (threadIdx.x >> 4) * S + static_cast<int>(rank); j < BN; j += (kSlThreads / 16) * S) {
+    const int t = tok0 + j;
+    if (t >= a.tokens) break;
+    const uint32_t at = area + static_cast<uint32_t>(j) * 512u + static_cast<uint32_t>(group) * 4u;
+    uint4 x[S][2], low[2];
+#pragma unroll
+    for (int p = 0; p < S; ++p) {
+      const uint32_t from = mapa_shared(at, p);
+      x[p][0] = ld_cluster_u4(from);
+      x[p][1] = ld_cluster_u4(from + 16);
+    }
+    if (ext_any) {
+      const uint32_t from = mapa_shared(at + BN * 512u, S - 1);
+      low[0] = ld_cluster_u4(from);
+      low[1] = ld_cluster_u4(from + 16);
+    }
+    float o[8];
+    if (I8) {
+      int sum[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] = 0;
+#pragma unroll
+      for (int p = 0; p < S; ++p) {
+        const uint32_t w[8] = {x[p][0].x, x[p][0].y, x[p][0].z, x[p][0].w, x[p][1].x, x[p][1].y, x[p][1].z, x[p][1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += static_cast<int>(w[e]);
+      }
+      const float sx = sxs[j];
+      const uint32_t w[8] = {low[0].x, low[0].y, low[0].z, low[0].w, low[1].x, low[1].y, low[1].z, low[1].w};
+      // as linear_i8_pair_kernel's epilogue, operation by operation
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float c = ext_any ? fmaf(g[e], __uint_as_float(w[e]), b[e]) : b[e];
+        o[e] = fmaf(static_cast<float>(sum[e]) * sx, swg[e], c);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int p = 0; p < S; ++p) {
+        const uint32_t w[8] = {x[p][0].x, x[p][0].y, x[p][0].z, x[p][0].w, x[p][1].x, x[p][1].y, x[p][1].z, x[p][1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += __uint_as_float(w[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] *= a.alpha;
+    }
+    uint4 pk;
+    pk.x = pack_bf16x2(o[0], o[1]);
+    pk.y = pack_bf16x2(o[2], o[3]);
+    pk.z = pack_bf16x2(o[4], o[5]);
+    pk.w = pack_bf16x2(o[6], o[7]);
+    const long long off = static_cast<long long>(t) * a.rows + row0 + group;
+    *reinterpret_cast<uint4*>(a.out + off) = pk;
+    if (!I8 && a.out_lo) {
+      uint4 lo;
+      lo.x = pack_bf16x2(o[0] - bf16_lo(pk.x), o[1] - bf16_hi(pk.x));
+      lo.y = pack_bf16x2(o[2] - bf16_lo(pk.y), o[3] - bf16_hi(pk.y));
+      lo.z = pack_bf16x2(o[4] - bf16_lo(pk.z), o[5] - bf16_hi(pk.z));
+      lo.w = pack_bf16x2(o[6] - bf16_lo(pk.w), o[7] - bf16_hi(pk.w));
+      *reinterpret_cast<uint4*>(a.out_lo + off) = lo;
+    }
+  }
+}
+
 // I8: out = bf16(b + g * (sx sw * (W_q x_q^T) + B P^T)), tmW/tmX int8 and
 // tmB/tmP the adapter's; else out = bf16(alpha * W x^T), all bf16.
 template <bool I8, int BN>
@@ -80,16 +170,17 @@ __global__ void __launch_bounds__(kSlThreads)
     linear_slice_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmP,
                         const SliceArgs a) {
-  constexpr int kStages = slice_stages(BN);
+  constexpr int kStages = slice_stages(I8, BN);
   constexpr uint32_t kStageBytes = slice_stage_bytes(BN);
-  constexpr int kCh = BN < kSlChunk ? BN : kSlChunk;
   constexpr uint32_t kColsTmem = I8 ? 2 * BN : (BN < 32 ? 32 : BN);
-  static_assert(kStages * kStageBytes >= 2 * kCh * 512, "the exchange fits in the ring");
+  static_assert(kStages * kStageBytes >= (I8 ? 2 : 1) * BN * 512, "the exchange fits in the ring");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t base_s = (raw_s + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base_s - raw_s);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  float* rowf = reinterpret_cast<float*>(smem + kStages * kStageBytes);  // sw * g, g, b of the tile's rows
+  float* sxs = rowf + 3 * kLinBM;                                        // the tokens' scales
+  uint64_t* full = reinterpret_cast<uint64_t*>(sxs + 128);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
@@ -192,37 +283,31 @@ __global__ void __launch_bounds__(kSlThreads)
   __syncwarp();
 
   // ---------------------------------------------------------------- exchange
-  const int et = static_cast<int>(threadIdx.x) - 64;  // epilogue thread
-  const int group = (et & 15) * 8;                    // its eight rows of the tile
-  const bool group_ok = et >= 0 && row0 + group < a.rows;
-  float g[8], sw[8], b[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    g[e] = 1.f;
-    sw[e] = b[e] = 0.f;
-    if (I8 && group_ok) {
-      const int c = row0 + group + e;
-      g[e] = a.m ? __ldg(a.m + c) / __ldg(a.n + c) : 1.f;
-      sw[e] = __ldg(a.w_scale + c) * g[e];
-      if (a.bias) b[e] = __bfloat162float(a.bias[c]);
+  const bool ext_any = I8 && a.kb_total > a.kb_main;
+  if (warp >= 2) {
+    const int q = warp & 3;  // TMEM lane quarter
+    if (I8) {
+      const int et = static_cast<int>(threadIdx.x) - 64, c = row0 + et;
+      float g = 0.f, sw = 0.f, b = 0.f;
+      if (c < a.rows) {
+        g = a.m ? __ldg(a.m + c) / __ldg(a.n + c) : 1.f;
+        sw = __ldg(a.w_scale + c) * g;
+        if (a.bias) b = __bfloat162float(a.bias[c]);
+      }
+      rowf[et] = sw;
+      rowf[kLinBM + et] = g;
+      rowf[2 * kLinBM + et] = b;
+      if (et < BN) sxs[et] = tok0 + et < a.tokens ? __ldg(a.x_scale + tok0 + et) : 0.f;
     }
-  }
-  bool alive = true;
-  if (et >= 0) {
-    alive = mbar_wait_warp(acc_full, 0, limit);
+    const bool alive = mbar_wait_warp(acc_full, 0, limit);
     if (!alive && lane == 0) atomicExch(a.status, 5);
     tc_fence_after();
-  }
-  const int q = warp & 3;
-  const bool ext_any = I8 && a.kb_total > a.kb_main;
-#pragma unroll 1
-  for (int c0 = 0; c0 < BN; c0 += kCh) {
-    if (tok0 + c0 >= a.tokens) break;  // the same for the whole cluster
-    if (et >= 0 && alive) {
-      const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + c0;
+    if (alive) {
+      const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
       uint32_t* dst = reinterpret_cast<uint32_t*>(smem) + q * 32 + lane;
-#pragma unroll
-      for (int j = 0; j < kCh; j += 16) {
+#pragma unroll 4
+      for (int j = 0; j < BN; j += 16) {
+        if (tok0 + j >= a.tokens) break;  // warp-uniform
         uint32_t u[16];
         tmem_ld16(lane_addr + j, u);
 #pragma unroll
@@ -230,80 +315,23 @@ __global__ void __launch_bounds__(kSlThreads)
         if (has_ext) {
           tmem_ld16(lane_addr + BN + j, u);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) dst[(kCh + j + e) * 128] = u[e];
+          for (int e = 0; e < 16; ++e) dst[(BN + j + e) * 128] = u[e];
         }
       }
     }
-    cluster_sync_all();
-    if (group_ok) {
-      for (int i = et >> 4; i * static_cast<int>(splits) + static_cast<int>(rank) < kCh; i += 8) {
-        const int j = i * static_cast<int>(splits) + static_cast<int>(rank);
-        const int t = tok0 + c0 + j;
-        if (t >= a.tokens) break;
-        const uint32_t at = base_s + static_cast<uint32_t>(j) * 512u + static_cast<uint32_t>(group) * 4u;
-        float o[8];
-        if (I8) {
-          int sum[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] = 0;
-          for (uint32_t p = 0; p < splits; ++p) {
-            const uint32_t from = mapa_shared(at, p);
-            const uint4 x = ld_cluster_u4(from), y = ld_cluster_u4(from + 16);
-            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += static_cast<int>(w[e]);
-          }
-          const float sx = __ldg(a.x_scale + t);
-          float low[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) low[e] = b[e];
-          if (ext_any) {
-            const uint32_t from = mapa_shared(at + kCh * 512u, splits - 1);
-            const uint4 x = ld_cluster_u4(from), y = ld_cluster_u4(from + 16);
-            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) low[e] = fmaf(g[e], __uint_as_float(w[e]), b[e]);
-          }
-          // as linear_i8_pair_kernel's epilogue, operation by operation
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = fmaf(static_cast<float>(sum[e]) * sx, sw[e], low[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = 0.f;
-          for (uint32_t p = 0; p < splits; ++p) {
-            const uint32_t from = mapa_shared(at, p);
-            const uint4 x = ld_cluster_u4(from), y = ld_cluster_u4(from + 16);
-            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] += __uint_as_float(w[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] *= a.alpha;
-        }
-        uint4 pk;
-        pk.x = pack_bf16x2(o[0], o[1]);
-        pk.y = pack_bf16x2(o[2], o[3]);
-        pk.z = pack_bf16x2(o[4], o[5]);
-        pk.w = pack_bf16x2(o[6], o[7]);
-        const long long off = static_cast<long long>(t) * a.rows + row0 + group;
-        *reinterpret_cast<uint4*>(a.out + off) = pk;
-        if (!I8 && a.out_lo) {
-          uint4 lo;
-          lo.x = pack_bf16x2(o[0] - bf16_lo(pk.x), o[1] - bf16_hi(pk.x));
-          lo.y = pack_bf16x2(o[2] - bf16_lo(pk.y), o[3] - bf16_hi(pk.y));
-          lo.z = pack_bf16x2(o[4] - bf16_lo(pk.z), o[5] - bf16_hi(pk.z));
-          lo.w = pack_bf16x2(o[6] - bf16_lo(pk.w), o[7] - bf16_hi(pk.w));
-          *reinterpret_cast<uint4*>(a.out_lo + off) = lo;
-        }
-      }
-    }
-    __syncwarp();
-    cluster_sync_all();  // the next chunk, or the end, may not overtake a reader of this CTA's memory
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();
+  switch (splits) {
+    case 1: slice_join<I8, BN, 1>(a, base_s, rowf, sxs, rank, row0, tok0, ext_any); break;
+    case 2: slice_join<I8, BN, 2>(a, base_s, rowf, sxs, rank, row0, tok0, ext_any); break;
+    case 4: slice_join<I8, BN, 4>(a, base_s, rowf, sxs, rank, row0, tok0, ext_any); break;
+    default: slice_join<I8, BN, 8>(a, base_s, rowf, sxs, rank, row0, tok0, ext_any); break;
+  }
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kColsTmem);
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves while another reads its exchange area
 }
 
 }  // namespace dora
