@@ -174,7 +174,7 @@ int device_info(DeviceInfo** out) {
     for (int i8 = 0; i8 < 2; ++i8)
       for (int bn : {16, 32, 64, 128})
         if (cudaFuncSetAttribute(slice_kernel(i8 != 0, bn), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(slice_smem(i8 != 0, bn))) != cudaSuccess ||
+                                 static_cast<int>(kSlSmemOne)) != cudaSuccess ||
             cudaFuncSetAttribute(slice_kernel(i8 != 0, bn), cudaFuncAttributePreferredSharedMemoryCarveout,
                                  cudaSharedmemCarveoutMaxShared) != cudaSuccess)
           return DORA_ERR_CUDA;
@@ -948,14 +948,18 @@ constexpr int64_t kSliceTokens = 128;
 int slice_bn(int64_t tokens) { return tokens <= 16 ? 16 : (tokens <= 32 ? 32 : (tokens <= 64 ? 64 : 128)); }
 
 // One slice launch over `a`: K split over as many CTAs of a cluster as keep
-// the grid within what is resident at once.
+// the grid within `room` CTAs (0: what is resident at once).
 int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const CUtensorMap& tmB,
-                 const CUtensorMap& tmP, SliceArgs a, bool after, const DeviceInfo* dev, cudaStream_t st) {
+                 const CUtensorMap& tmP, SliceArgs a, bool after, long long room, const DeviceInfo* dev,
+                 cudaStream_t st) {
   const int bn = slice_bn(a.tokens);
   const long long row_tiles = cdiv(a.rows, kLinBM), tok_tiles = cdiv(a.tokens, bn);
-  const long long most = static_cast<long long>(slice_ctas(i8, bn)) * dev->num_sms;
+  const bool one = (i8 && bn > 64) || room > 0;  // a CTA an SM
+  if (room == 0) room = (one ? 1LL : 2LL) * dev->num_sms;
   int splits = 1;
-  while (splits < 8 && 2 * splits <= a.kb_main && 2 * row_tiles * tok_tiles * splits <= most) splits *= 2;
+  while (splits < 8 && 2 * splits <= a.kb_main && 2 * row_tiles * tok_tiles * splits <= room) splits *= 2;
+  const size_t smem = one ? kSlSmemOne : kSlSmemTwo;
+  a.stages = static_cast<int>(std::min<size_t>(kSlMaxStages, (smem - kSlFixed) / slice_stage_bytes(bn)));
   a.wait_limit = kWaitLimitCycles;
   a.status = dev->status;
   cudaLaunchAttribute attrs[2];
@@ -970,7 +974,7 @@ int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const 
   cfg.attrs = attrs;
   cfg.numAttrs = after ? 2 : 1;
   cfg.blockDim = dim3(kSlThreads);
-  cfg.dynamicSmemBytes = slice_smem(i8, bn);
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = dim3(static_cast<unsigned>(row_tiles * splits), static_cast<unsigned>(tok_tiles));
   note_launch();
   return cudaLaunchKernelEx(&cfg, slice_kernel(i8, bn), tmW, tmX, tmB, tmP, a) == cudaSuccess ? DORA_OK
@@ -978,9 +982,15 @@ int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const 
 }
 
 // P = bf16(s * x A^T), and what the rounding leaves unless P_lo is null, on
-// slices: few rank rows make few large tiles, so K is split instead.
+// slices: few rank rows make few large tiles, so K is split instead.  The
+// product behind it starts at once and takes the SMs that this grid leaves, but
+// its pairs share none with a CTA of this one: where that product's `pairs`
+// leave SMs idle (one wave), P keeps to those if its tiles fit there (1000
+// tokens through 4096 x 4096 at rank 64: 42.2 us, 46.2 with P on 64 SMs).
 int launch_p_slice(const void* x, const void* A, __nv_bfloat16* P, __nv_bfloat16* P_lo, float s, int64_t tokens,
-                   int64_t d_in, int64_t r, const DeviceInfo* dev, cudaStream_t st) {
+                   int64_t d_in, int64_t r, long long pairs, const DeviceInfo* dev, cudaStream_t st) {
+  const long long spare = dev->num_sms - 2 * std::min<long long>(pairs, dev->pair_clusters);
+  const bool beside = pairs > 0 && cdiv(r, kLinBM) * cdiv(tokens, slice_bn(tokens)) <= spare;
   CUtensorMap tmX, tmA;
   if (make_map(&tmA, A, r, d_in) || make_map(&tmX, x, tokens, d_in, slice_bn(tokens))) return DORA_ERR_CUDA;
   SliceArgs sa{};
@@ -990,7 +1000,7 @@ int launch_p_slice(const void* x, const void* A, __nv_bfloat16* P, __nv_bfloat16
   sa.alpha = s;
   sa.out = P;
   sa.out_lo = P_lo;
-  return launch_slice(false, tmA, tmX, tmA, tmX, sa, false, dev, st);
+  return launch_slice(false, tmA, tmX, tmA, tmX, sa, false, beside ? spare : 0, dev, st);
 }
 
 int fused_linear(const void* x, const void* W, const void* A, const void* B, const void* bias, const float* m,
@@ -1032,7 +1042,8 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
   cudaLaunchAttribute attrs[2];
   if (ckpt) {
     __nv_bfloat16* P_lo = r > 0 ? P + p_bytes / 2 : nullptr;
-    if (r > 0 && launch_p_slice(x, A, P, P_lo, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
+    if (r > 0 && launch_p_slice(x, A, P, P_lo, s, tokens, d_in, r, tiles_m2 * cdiv(d_out, kPairBN), dev, st))
+      return DORA_ERR_CUDA;
     CUtensorMap tmLo;
     if (r > 0 && make_map(&tmLo, P_lo, tokens, r)) return DORA_ERR_CUDA;
     LinearCkptArgs ca{};
@@ -1315,7 +1326,7 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
     SliceArgs sa{};
     sa.tokens = static_cast<int>(tokens);
     if (r > 0 && (make_map(&tmB, B, d_out, r) || make_map(&tmP, P, tokens, r, bn) ||
-                  launch_p_slice(x, A, P, nullptr, s, tokens, d_in, r, dev, st)))
+                  launch_p_slice(x, A, P, nullptr, s, tokens, d_in, r, 0, dev, st)))
       return DORA_ERR_CUDA;
     sa.rows = static_cast<int>(d_out);
     sa.kb_main = static_cast<int>(cdiv(d_in, kI8BK));
@@ -1326,12 +1337,12 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
     sa.n = n;
     sa.bias = static_cast<const __nv_bfloat16*>(bias);
     sa.out = static_cast<__nv_bfloat16*>(y);
-    return launch_slice(true, tmWq, tmXq, r > 0 ? tmB : tmWq, r > 0 ? tmP : tmXq, sa, r > 0, dev, st);
+    return launch_slice(true, tmWq, tmXq, r > 0 ? tmB : tmWq, r > 0 ? tmP : tmXq, sa, r > 0, 0, dev, st);
   }
   if (make_map_i8(&tmXq, x_q, tokens, d_in, kLinBM) || make_map_i8(&tmWq, W_q, d_out, d_in, kPairBN / 2))
     return DORA_ERR_CUDA;
   if (r > 0 && (make_map(&tmP, P, tokens, r) || make_map(&tmB, B, d_out, r, kPairBN / 2) ||
-                launch_p_slice(x, A, P, nullptr, s, tokens, d_in, r, dev, st)))
+                launch_p_slice(x, A, P, nullptr, s, tokens, d_in, r, cdiv(tokens, kPairBM) * cdiv(d_out, kPairBN), dev, st)))
     return DORA_ERR_CUDA;
   LinearI8Args la{};
   la.M = static_cast<int>(tokens);

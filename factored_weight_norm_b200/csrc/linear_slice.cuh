@@ -27,23 +27,18 @@ constexpr int kSlMaxStages = 8;
 // alignment; row factors (sw * g, g, b) and token scales; barriers
 constexpr size_t kSlFixed = 1024 + (3 * kLinBM + 128) * 4 + 256;
 
-// CTAs an SM and their shared memory: two, but one for the product of 128
-// tokens, whose exchange (int32 sums and the adapter's fp32 beside them) takes
-// 128 KB.
-__host__ __device__ constexpr int slice_ctas(bool i8, int bn) { return i8 && bn > 64 ? 1 : 2; }
-__host__ __device__ constexpr size_t slice_smem(bool i8, int bn) {
-  return slice_ctas(i8, bn) == 2 ? 112 * 1024 : 200 * 1024;
-}
+// Shared memory of a CTA: two fit on an SM, or one with a ring of twice the
+// depth (200 KB): for the product of 128 tokens, whose exchange (int32 sums and
+// the adapter's fp32 beside them) takes 128 KB, and for a grid so small that
+// its CTAs have an SM each anyway.
+constexpr size_t kSlSmemTwo = 112 * 1024, kSlSmemOne = 200 * 1024;
 __host__ __device__ constexpr uint32_t slice_stage_bytes(int bn) { return kLinABytes + bn * 128u; }
-__host__ __device__ constexpr int slice_stages(bool i8, int bn) {
-  const int n = static_cast<int>((slice_smem(i8, bn) - kSlFixed) / slice_stage_bytes(bn));
-  return n < kSlMaxStages ? n : kSlMaxStages;
-}
 
 struct SliceArgs {
   int rows;               // weight rows (d_out; r for the down projection)
   int tokens;
   int kb_main, kb_total;  // K blocks; total with the adapter's
+  int stages;             // of the ring
   const float* x_scale;   // I8: as in LinearI8Args
   const float* w_scale;
   const float* m;
@@ -170,19 +165,18 @@ __global__ void __launch_bounds__(kSlThreads)
     linear_slice_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmP,
                         const SliceArgs a) {
-  constexpr int kStages = slice_stages(I8, BN);
   constexpr uint32_t kStageBytes = slice_stage_bytes(BN);
   constexpr uint32_t kColsTmem = I8 ? 2 * BN : (BN < 32 ? 32 : BN);
-  static_assert(kStages * kStageBytes >= (I8 ? 2 : 1) * BN * 512, "the exchange fits in the ring");
+  const int stages = a.stages;  // the host's: the exchange fits in the ring
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t base_s = (raw_s + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base_s - raw_s);
-  float* rowf = reinterpret_cast<float*>(smem + kStages * kStageBytes);  // sw * g, g, b of the tile's rows
+  float* rowf = reinterpret_cast<float*>(smem + stages * kStageBytes);  // sw * g, g, b of the tile's rows
   float* sxs = rowf + 3 * kLinBM;                                        // the tokens' scales
   uint64_t* full = reinterpret_cast<uint64_t*>(sxs + 128);
-  uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;
+  uint64_t* empty = full + stages;
+  uint64_t* acc_full = empty + stages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -198,7 +192,7 @@ __global__ void __launch_bounds__(kSlThreads)
   const long long limit = a.wait_limit;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -222,26 +216,31 @@ __global__ void __launch_bounds__(kSlThreads)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int filled = 0;
+      int stage = 0, filled = 0;
+      uint32_t phase = 0;
       for (int kb = kb0; kb < kb1; ++kb, ++filled) {
-        const int s = filled % kStages;
         const bool ext = I8 && kb >= a.kb_main;
         if (ext && kb == a.kb_main) {
           grid_dep_wait();  // P comes from the launch before
           fence_proxy_async_all();
         }
-        if (!mbar_wait(&empty[s], static_cast<uint32_t>(filled / kStages & 1) ^ 1u, limit)) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, limit)) {
           atomicExch(a.status, 5);  // DORA_ERR_TIMEOUT
           break;
         }
-        mbar_arrive_expect_tx(&full[s], kStageBytes);
+        mbar_arrive_expect_tx(&full[stage], kStageBytes);
         const int xk = I8 && !ext ? kb * kI8BK : (ext ? kb - a.kb_main : kb) * kLinBK;
-        tma_load_2d(base_s + s * kStageBytes, ext ? &tmB : &tmW, &full[s], xk, row0);
-        tma_load_2d(base_s + s * kStageBytes + kLinABytes, ext ? &tmP : &tmX, &full[s], xk, tok0);
+        const uint32_t dst = base_s + stage * kStageBytes;
+        tma_load_2d(dst, ext ? &tmB : &tmW, &full[stage], xk, row0);
+        tma_load_2d(dst + kLinABytes, ext ? &tmP : &tmX, &full[stage], xk, tok0);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
       // never leave a TMA copy in flight: the last fill of every stage
-      for (int f = max(0, filled - kStages); f < filled; ++f)
-        mbar_wait(&full[f % kStages], static_cast<uint32_t>(f / kStages & 1), limit);
+      for (int f = max(0, filled - stages); f < filled; ++f)
+        mbar_wait(&full[f % stages], static_cast<uint32_t>(f / stages & 1), limit);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
@@ -250,16 +249,16 @@ __global__ void __launch_bounds__(kSlThreads)
       const uint32_t idesc_e = idesc_bf16_f32(kLinBM, BN);
       const uint64_t desc0 = sw128_kmajor_desc(base_s);
       bool ok = true;
-      int it = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % kStages;
-        if (!mbar_wait(&full[s], static_cast<uint32_t>(it / kStages & 1), limit)) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&full[stage], phase, limit)) {
           atomicExch(a.status, 5);
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint64_t ad = desc0 + static_cast<uint64_t>(s) * (kStageBytes >> 4);
+        const uint64_t ad = desc0 + static_cast<uint64_t>(stage) * (kStageBytes >> 4);
         const uint64_t bd = ad + (kLinABytes >> 4);
         const bool ext = I8 && kb >= a.kb_main;
         const uint32_t first = ext ? a.kb_main : kb0;
@@ -273,7 +272,11 @@ __global__ void __launch_bounds__(kSlThreads)
           else
             mma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc_m, acc);
         }
-        mma_commit(&empty[s]);
+        mma_commit(&empty[stage]);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
       // after a wait that gave up the MMAs already issued must still end before TMEM is freed
       mma_commit(acc_full);
