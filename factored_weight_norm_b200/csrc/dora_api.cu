@@ -948,7 +948,10 @@ constexpr int64_t kSliceTokens = 128;
 int slice_bn(int64_t tokens) { return tokens <= 16 ? 16 : (tokens <= 32 ? 32 : (tokens <= 64 ? 64 : 128)); }
 
 // One slice launch over `a`: K split over as many CTAs of a cluster as keep
-// the grid within `room` CTAs (0: what is resident at once).
+// the grid within `room` CTAs (0: what is resident at once), with eight K blocks
+// each at least: 64 tokens through 4096 x 2048 took 18.0 us in eighths of four
+// blocks, 14.2 in quarters.  A product of 64 tokens and more takes at most four:
+// its join reads every split's tile (8192 x 4096: 21.6 us, 24.6 in eighths).
 int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const CUtensorMap& tmB,
                  const CUtensorMap& tmP, SliceArgs a, bool after, long long room, const DeviceInfo* dev,
                  cudaStream_t st) {
@@ -957,7 +960,7 @@ int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const 
   const bool one = (i8 && bn > 64) || room > 0;  // a CTA an SM
   if (room == 0) room = (one ? 1LL : 2LL) * dev->num_sms;
   int splits = 1;
-  while (splits < 8 && 2 * splits <= a.kb_main && 2 * row_tiles * tok_tiles * splits <= room) splits *= 2;
+  while (splits < (i8 && bn >= 64 ? 4 : 8) && 16 * splits <= a.kb_main && 2 * row_tiles * tok_tiles * splits <= room) splits *= 2;
   const size_t smem = one ? kSlSmemOne : kSlSmemTwo;
   a.stages = static_cast<int>(std::min<size_t>(kSlMaxStages, (smem - kSlFixed) / slice_stage_bytes(bn)));
   a.wait_limit = kWaitLimitCycles;
@@ -1339,18 +1342,23 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
     sa.out = static_cast<__nv_bfloat16*>(y);
     return launch_slice(true, tmWq, tmXq, r > 0 ? tmB : tmWq, r > 0 ? tmP : tmXq, sa, r > 0, 0, dev, st);
   }
-  if (make_map_i8(&tmXq, x_q, tokens, d_in, kLinBM) || make_map_i8(&tmWq, W_q, d_out, d_in, kPairBN / 2))
-    return DORA_ERR_CUDA;
-  if (r > 0 && (make_map(&tmP, P, tokens, r) || make_map(&tmB, B, d_out, r, kPairBN / 2) ||
-                launch_p_slice(x, A, P, nullptr, s, tokens, d_in, r, cdiv(tokens, kPairBM) * cdiv(d_out, kPairBN), dev, st)))
+  // 128-wide tiles take 0.58 of a 256-wide one's time: the width whose waves over
+  // the pairs end first
+  const long long tiles_m = cdiv(tokens, kPairBM);
+  const auto waves = [&](int width) { return cdiv(tiles_m * cdiv(d_out, width), dev->pair_clusters); };
+  const int bn = 58 * waves(128) < 100 * waves(256) ? 128 : 256;
+  if (make_map_i8(&tmXq, x_q, tokens, d_in, kLinBM) || make_map_i8(&tmWq, W_q, d_out, d_in, bn / 2)) return DORA_ERR_CUDA;
+  if (r > 0 && (make_map(&tmP, P, tokens, r) || make_map(&tmB, B, d_out, r, bn / 2) ||
+                launch_p_slice(x, A, P, nullptr, s, tokens, d_in, r, tiles_m * cdiv(d_out, bn), dev, st)))
     return DORA_ERR_CUDA;
   LinearI8Args la{};
   la.M = static_cast<int>(tokens);
   la.N = static_cast<int>(d_out);
   la.kb_main = static_cast<int>(cdiv(d_in, kI8BK));
   la.kb_total = la.kb_main + static_cast<int>(cdiv(r, kLinBK));
-  la.tiles_m = static_cast<int>(cdiv(tokens, kPairBM));
-  la.tiles_n = static_cast<int>(cdiv(d_out, kPairBN));
+  la.tiles_m = static_cast<int>(tiles_m);
+  la.tiles_n = static_cast<int>(cdiv(d_out, bn));
+  la.bn = bn;
   la.stages = linear_i8_stages(dev->smem_optin);
   la.x_scale = x_scale;
   la.w_scale = w_scale;

@@ -34,6 +34,7 @@ struct LinearI8Args {
   int M, N;              // tokens and output channels
   int kb_main, kb_total; // K blocks of the int8 operands; total with the adapter's
   int tiles_m, tiles_n;
+  int bn;                // pair tile width along N: 256 or 128
   int stages;
   const float* x_scale;  // [M]
   const float* w_scale;  // [N]
@@ -100,7 +101,9 @@ __device__ __forceinline__ void quad_store(uint8_t* at, long long pitch, const u
 // eight epilogue warps (two per lane quarter, 128 columns each) first pull
 // their whole base part into registers and release it, then finish the tile
 // beside the next main loop.  The next adapter product comes last in its tile,
-// long after its accumulator has been read.
+// long after its accumulator has been read.  Tiles of 128 channels (each warp
+// then has 64 of them) serve products whose 256-wide tiles leave half of the
+// pairs without one.
 __global__ void __launch_bounds__(kI8Threads, 1)
     linear_i8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                           const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmB,
@@ -128,6 +131,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const long long limit = a.wait_limit;
   const int n_tiles = a.tiles_m * a.tiles_n;
   const bool has_ext = a.kb_total > a.kb_main;
+  // bytes that both CTAs' copies bring per stage
+  const uint32_t stage_tx = 2 * kPairKps * (kLinABytes + a.bn / 2 * 128u);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         int tm, tn;
         lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
         const int yx = tm * kPairBM + static_cast<int>(rank) * kLinBM;
-        const int yw = tn * kPairBN + static_cast<int>(rank) * (kPairBN / 2);
+        const int yw = tn * a.bn + static_cast<int>(rank) * (a.bn / 2);
         for (int kb0 = 0; kb0 < a.kb_total; kb0 += kPairKps) {
           if (kb0 + kPairKps > a.kb_main && !ext_ready) {
             grid_dep_wait();  // P comes from the launch before
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           bool got = true;
           if (lane == 0) {
             got = mbar_wait(&empty[stage], phase ^ 1u, limit);
-            if (got && leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
+            if (got && leader) mbar_arrive_expect_tx(&full[stage], stage_tx);
             if (!got) lin_timeout(a.status, abort_flag);
           }
           got = __shfl_sync(0xffffffffu, got, 0);
@@ -220,8 +225,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t idesc_b = idesc_i8_s32(kPairBM, kPairBN);
-        const uint32_t idesc_e = idesc_bf16_f32(kPairBM, kPairBN);
+        const uint32_t idesc_b = idesc_i8_s32(kPairBM, a.bn);
+        const uint32_t idesc_e = idesc_bf16_f32(kPairBM, a.bn);
         const uint64_t desc0 = sw128_kmajor_desc(base_s);
         const uint64_t desc_step = kPairStageBytes >> 4;
         uint32_t it = 0;
@@ -279,9 +284,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     regs_take<kI8RegsMany>();
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    const int half = (warp - 4) >> 2;  // columns half * 128 .. of the tile
+    const int width = a.bn / 2;
+    const int first = ((warp - 4) >> 2) * width;  // columns first .. first + width - 1 of the tile
     const int et = threadIdx.x - 128;
-    const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+    const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + first;
     const uint32_t base_empty_leader = mapa_shared(smem_u32(base_empty), 0);
     const uint32_t ext_empty_leader = mapa_shared(smem_u32(ext_empty), 0);
     uint32_t it = 0;
@@ -293,9 +299,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       // read by warps finishing the tile before
       float* cf = cols + (it & 1u) * 3 * kPairBN;
       {
-        const int c = tn * kPairBN + et;
+        const int c = tn * a.bn + et;
         float g = 0.f, sw = 0.f, b = 0.f;
-        if (c < a.N) {
+        if (et < a.bn && c < a.N) {
           g = a.m ? __ldg(a.m + c) / __ldg(a.n + c) : 1.f;
           sw = __ldg(a.w_scale + c);
           if (a.bias) b = __bfloat162float(a.bias[c]);
@@ -319,16 +325,17 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(base_empty_leader);
-      const int col0 = tn * kPairBN + half * 128;
-      const float* swg = cf + half * 128;
+      const int col0 = tn * a.bn + first;
+      const float* swg = cf + first;
       const int piece = lane & 3;
       const long long row4 = row - piece;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
+        if (c * 32 >= width) break;
         float u[32];
         if (has_ext) {
           tmem_ld32(tmem_lane + kPairBN + c * 32, u);
-          if (c == 3) {
+          if (c == 3 || (c + 1) * 32 == width) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(ext_empty_leader);

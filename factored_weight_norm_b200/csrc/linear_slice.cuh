@@ -191,6 +191,17 @@ __global__ void __launch_bounds__(kSlThreads)
   const bool has_ext = I8 && kb1 > a.kb_main;
   const long long limit = a.wait_limit;
 
+  // K block kb into a stage of the ring
+  const auto fill = [&](int stage, int kb) {
+    const bool ext = I8 && kb >= a.kb_main;
+    mbar_arrive_expect_tx(&full[stage], kStageBytes);
+    const int xk = I8 && !ext ? kb * kI8BK : (ext ? kb - a.kb_main : kb) * kLinBK;
+    const uint32_t dst = base_s + stage * kStageBytes;
+    tma_load_2d(dst, ext ? &tmB : &tmW, &full[stage], xk, row0);
+    tma_load_2d(dst + kLinABytes, ext ? &tmP : &tmX, &full[stage], xk, tok0);
+  };
+  // the first fills wait for nothing, so they go out before the rest is set up
+  const int early = min(stages, min(kb1, a.kb_main) - kb0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
@@ -198,10 +209,7 @@ __global__ void __launch_bounds__(kSlThreads)
     }
     mbar_init(acc_full, 1);
     fence_mbar_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmX);
+    for (int s = 0; s < early; ++s) fill(s, kb0 + s);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, kColsTmem);
@@ -216,11 +224,10 @@ __global__ void __launch_bounds__(kSlThreads)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int stage = 0, filled = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++filled) {
-        const bool ext = I8 && kb >= a.kb_main;
-        if (ext && kb == a.kb_main) {
+      int filled = early, stage = early == stages ? 0 : early;
+      uint32_t phase = early == stages ? 1u : 0u;
+      for (int kb = kb0 + early; kb < kb1; ++kb, ++filled) {
+        if (I8 && kb == a.kb_main) {
           grid_dep_wait();  // P comes from the launch before
           fence_proxy_async_all();
         }
@@ -228,11 +235,7 @@ __global__ void __launch_bounds__(kSlThreads)
           atomicExch(a.status, 5);  // DORA_ERR_TIMEOUT
           break;
         }
-        mbar_arrive_expect_tx(&full[stage], kStageBytes);
-        const int xk = I8 && !ext ? kb * kI8BK : (ext ? kb - a.kb_main : kb) * kLinBK;
-        const uint32_t dst = base_s + stage * kStageBytes;
-        tma_load_2d(dst, ext ? &tmB : &tmW, &full[stage], xk, row0);
-        tma_load_2d(dst + kLinABytes, ext ? &tmP : &tmX, &full[stage], xk, tok0);
+        fill(stage, kb);
         if (++stage == stages) {
           stage = 0;
           phase ^= 1u;

@@ -205,12 +205,14 @@ def _dense_cuda(*ts):
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("tensors must live on a CUDA device")
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.get_device() != cur:
-            raise ValueError(f"tensor on {t.device} but the current device is cuda:{cur}")
+        dev = t.get_device()  # -1 on the host
+        if dev != cur:
+            if dev < 0:
+                raise ValueError("tensors must live on a CUDA device")
+            if cur is None:
+                cur = torch.cuda.current_device()
+            if dev != cur:
+                raise ValueError(f"tensor on {t.device} but the current device is cuda:{cur}")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous (row-major)")
 
@@ -547,7 +549,7 @@ def dora_factored_norm_bwd(W, A, B, s: float, n, d_n, dA=None, dB=None, workspac
 # ---------------------------------------------------------- 8-bit operators
 def _typed(where: str, name: str, t, shape, dtype):
     """t (None skipped) has this shape and dtype."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape):
         return
     if t.shape != shape:
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -567,25 +569,28 @@ def _checkpoint(where, tokens, d_out, z8, z_scale, device):
     return z8, z_scale
 
 
-def _rows_i8(where, x, residual, h, q, scale):
-    _acts2d(x, where)
-    rows, cols = x.shape
-    _like(x, where, residual=residual, h=h)
-    _typed(where, "q", q, (rows, cols), torch.int8)
+def _rows_i8(where, x, residual, weight, h, y, q, scale):
+    """Checks the rows' operands and makes the outputs that are not given: (rows, cols, dt, h, q, scale)."""
+    if x.dim() != 2:
+        raise ValueError(f"{where}: activations must be 2-D [tokens, d_out], got {tuple(x.shape)}")
+    dt, shape, dtype = _dt(x), x.shape, x.dtype
+    rows, cols = shape
+    _typed(where, "residual", residual, shape, dtype)
+    _typed(where, "h", h, shape, dtype)
+    _typed(where, "y", y, shape, dtype)
+    _typed(where, "weight", weight, (cols,), dtype)
+    _typed(where, "q", q, shape, torch.int8)
     _typed(where, "scale", scale, (rows,), torch.float32)
     if h is not None and residual is None:
         raise ValueError(f"{where}: h is x + residual, so it needs a residual")
-
-
-def _rows_i8_outputs(x, residual, h, q, scale):
-    rows, cols = x.shape
+    _dense_cuda(x, residual, weight, h, y, q, scale)
     if residual is not None and h is None:
         h = torch.empty_like(x)
     if q is None:
-        q = torch.empty(rows, cols, dtype=torch.int8, device=x.device)
+        q = torch.empty_like(x, dtype=torch.int8)
     if scale is None:
         scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    return h, q, scale
+    return rows, cols, dt, h, q, scale
 
 
 def dora_quantize_rows_i8(x, residual=None, h=None, q=None, scale=None, stream=None):
@@ -594,12 +599,9 @@ def dora_quantize_rows_i8(x, residual=None, h=None, q=None, scale=None, stream=N
     h is written in x's type where there is a residual (it may be x or
     residual itself) and None without one (the codes are x's)."""
     where = "dora_quantize_rows_i8"
-    _rows_i8(where, x, residual, h, q, scale)
-    _dense_cuda(x, residual, h, q, scale)
-    h, q, scale = _rows_i8_outputs(x, residual, h, q, scale)
-    st = lib().dora_quantize_rows_i8(_ptr(x), _ptr(residual), x.shape[0], x.shape[1], _dt(x), _ptr(h), _ptr(q),
-                                     _ptr(scale), _stream(stream))
-    _check(st, where)
+    rows, cols, dt, h, q, scale = _rows_i8(where, x, residual, None, h, None, q, scale)
+    _check(lib().dora_quantize_rows_i8(_ptr(x), _ptr(residual), rows, cols, dt, _ptr(h), _ptr(q), _ptr(scale),
+                                       _stream(stream)), where)
     return q, scale, h
 
 
@@ -610,16 +612,13 @@ def dora_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, want_y: bool =
     h as in dora_quantize_rows_i8; y is the norm in x's type (the adapter
     branch's input), None unless it is passed or ``want_y`` is true."""
     where = "dora_rms_norm_i8"
-    _rows_i8(where, x, residual, h, q, scale)
-    _like(x, where, y=y)
-    _typed(where, "weight", weight, (x.shape[1],), x.dtype)
-    _dense_cuda(x, weight, residual, h, y, q, scale)
-    h, q, scale = _rows_i8_outputs(x, residual, h, q, scale)
+    if weight is None:
+        raise ValueError(f"{where}: a weight is required")
+    rows, cols, dt, h, q, scale = _rows_i8(where, x, residual, weight, h, y, q, scale)
     if y is None and want_y:
         y = torch.empty_like(x)
-    st = lib().dora_rms_norm_i8(_ptr(x), _ptr(residual), _ptr(weight), float(eps), x.shape[0], x.shape[1], _dt(x),
-                                _ptr(h), _ptr(y), _ptr(q), _ptr(scale), _stream(stream))
-    _check(st, where)
+    _check(lib().dora_rms_norm_i8(_ptr(x), _ptr(residual), _ptr(weight), eps, rows, cols, dt, _ptr(h), _ptr(y),
+                                  _ptr(q), _ptr(scale), _stream(stream)), where)
     return q, scale, h, y
 
 
@@ -630,17 +629,18 @@ def dora_dequantize_i8(q, scale, dtype: torch.dtype = torch.bfloat16, out=None, 
         raise ValueError(f"{where}: q must be 2-D [rows, cols], got {tuple(q.shape)}")
     rows, cols = q.shape
     block = 0 if scale.dim() == 1 else CKPT_BLOCK
-    _typed(where, "q", q, (rows, cols), torch.int8)
+    _typed(where, "q", q, q.shape, torch.int8)
     _typed(where, "scale", scale, (rows,) if block == 0 else (rows, -(-cols // CKPT_BLOCK)), torch.float32)
-    dt = out.dtype if out is not None else dtype
-    _typed(where, "out", out, (rows, cols), dt)
-    if dt not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"unsupported dtype {dt}: bf16 or fp32 only")
+    if out is not None:
+        dtype = out.dtype
+        _typed(where, "out", out, q.shape, dtype)
+    dt = DORA_BF16 if dtype is torch.bfloat16 else DORA_F32
+    if dt == DORA_F32 and dtype is not torch.float32:
+        raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32 only")
     _dense_cuda(q, scale, out)
     if out is None:
-        out = torch.empty(rows, cols, dtype=dt, device=q.device)
-    _check(lib().dora_dequantize_i8(_ptr(q), _ptr(scale), rows, cols, block, _dt(out), _ptr(out), _stream(stream)),
-           where)
+        out = torch.empty_like(q, dtype=dtype)
+    _check(lib().dora_dequantize_i8(_ptr(q), _ptr(scale), rows, cols, block, dt, _ptr(out), _stream(stream)), where)
     return out
 
 
