@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       }
       const long long row = static_cast<long long>(tm) * kPairBM + rank * kLinBM + q * 32 + lane;
       const int col0 = tn * kPairBN + half * 128;
+      uint32_t open = 0;  // groups of eight codes that fp32 leaves open
       if (alive && col0 < a.N) {  // warp-uniform
         // columns past N are sums of zero-filled operands: they do not count
         const uint32_t top = __float_as_uint(max_abs<128>(0.f, v));
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
               uint32_t qc[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) z[e] = v[k + e];
-              codes_of<8>(z, top, inv, qc);
+              if (!codes_fast<8>(z, inv, qc)) open |= 1u << (k / 8);
               const uint32_t lo = pack_codes(qc[0], qc[1], qc[2], qc[3]), hi = pack_codes(qc[4], qc[5], qc[6], qc[7]);
               uint4& zp = zk[(c & 1) * 2 + j / 2];
               if (j & 1) {
@@ -326,6 +327,29 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 }
             }
           }
+        }
+      }
+      // settled here, by one piece of code behind the stores, and stored again:
+      // inlined sixteen times it made the epilogue's code too long for the
+      // instruction cache
+      __syncwarp();  // the quad's stores come first
+      if (open != 0 && row < a.M) {
+        const uint32_t top = __float_as_uint(max_abs<128>(0.f, v));
+        const float inv = top_inverse(top);
+#pragma unroll 1
+        for (; open != 0; open &= open - 1) {
+          const int k = (__ffs(open) - 1) * 8;
+          float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          uint32_t qc[8];
+#pragma unroll
+          for (int g = 0; g < 16; ++g)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = k == g * 8 ? v[g * 8 + e] : z[e];
+          codes_fast<8>(z, inv, qc);
+          codes_settle<8>(z, top, inv, qc);
+          if (col0 + k < a.N)
+            *reinterpret_cast<uint2*>(a.z8 + row * a.N + col0 + k) = make_uint2(
+                pack_codes(qc[0], qc[1], qc[2], qc[3]), pack_codes(qc[4], qc[5], qc[6], qc[7]));
         }
       }
       __syncwarp();
