@@ -944,6 +944,11 @@ int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, f
 // Up to this many tokens the int8 linear runs on slices of the weight.
 constexpr int64_t kSliceTokens = 128;
 
+// Up to this many tokens the down projection runs on down_tokens_kernel (8192 x
+// 8192 at rank 384, the whole call: one token 19.7 us, 21.3 on slices; four
+// 21.8 and 22.1; five 23.8 and 22.3).
+constexpr int64_t kDownTokens = 4;
+
 // Token tile of the slice kernels.
 int slice_bn(int64_t tokens) { return tokens <= 16 ? 16 : (tokens <= 32 ? 32 : (tokens <= 64 ? 64 : 128)); }
 
@@ -994,6 +999,15 @@ int launch_p_slice(const void* x, const void* A, __nv_bfloat16* P, __nv_bfloat16
                    int64_t d_in, int64_t r, long long pairs, const DeviceInfo* dev, cudaStream_t st) {
   const long long spare = dev->num_sms - 2 * std::min<long long>(pairs, dev->pair_clusters);
   const bool beside = pairs > 0 && cdiv(r, kLinBM) * cdiv(tokens, slice_bn(tokens)) <= spare;
+  if (tokens <= kDownTokens && !P_lo) {
+    const auto* xb = static_cast<const __nv_bfloat16*>(x);
+    const auto* ab = static_cast<const __nv_bfloat16*>(A);
+    const auto kernel = tokens == 1 ? down_tokens_kernel<1> : (tokens == 2 ? down_tokens_kernel<2> : down_tokens_kernel<4>);
+    note_launch();
+    kernel<<<static_cast<unsigned>(r), kDownThreads, 0, st>>>(xb, ab, s, static_cast<int>(tokens),
+                                                              static_cast<int>(d_in), static_cast<int>(r), P);
+    return launch_error();
+  }
   CUtensorMap tmX, tmA;
   if (make_map(&tmA, A, r, d_in) || make_map(&tmX, x, tokens, d_in, slice_bn(tokens))) return DORA_ERR_CUDA;
   SliceArgs sa{};

@@ -19,6 +19,7 @@
 #pragma once
 
 #include "linear_i8.cuh"
+#include "quant8.cuh"
 
 namespace dora {
 
@@ -155,6 +156,56 @@ __device__ __forceinline__ void slice_join(const SliceArgs& a, uint32_t area, co
       lo.w = pack_bf16x2(o[6] - bf16_lo(pk.w), o[7] - bf16_hi(pk.w));
       *reinterpret_cast<uint4*>(a.out_lo + off) = lo;
     }
+  }
+}
+
+// P = bf16(alpha * x A^T) for up to TOK tokens: one CTA per rank row, each
+// thread eight columns at a time, fp32 sums joined in a fixed order.  The
+// product behind it streams the base weight at the same time, and a slice
+// kernel's 24 CTAs get little of the memory's attention beside its 256 (6 MB
+// of A took 13 us, and the product then waited); these CTAs are many and small,
+// and fit beside the product's.
+constexpr int kDownThreads = 256;
+template <int TOK>
+__global__ void __launch_bounds__(kDownThreads) down_tokens_kernel(const __nv_bfloat16* __restrict__ x,
+                                                                   const __nv_bfloat16* __restrict__ A, float alpha,
+                                                                   int tokens, int d_in, int r,
+                                                                   __nv_bfloat16* __restrict__ P) {
+  __shared__ float part[kDownThreads / 32][TOK];
+  grid_dep_launch();
+  const __nv_bfloat16* row = A + static_cast<long long>(blockIdx.x) * d_in;
+  float acc[TOK];
+#pragma unroll
+  for (int t = 0; t < TOK; ++t) acc[t] = 0.f;
+#pragma unroll 4
+  for (int k = threadIdx.x * 8; k < d_in; k += kDownThreads * 8) {
+    float w[8];
+    VecIO<__nv_bfloat16, 8>::unpack(ld_stream_u4(row + k), w);
+#pragma unroll
+    for (int t = 0; t < TOK; ++t) {
+      if (t < tokens) {
+        float v[8];
+        VecIO<__nv_bfloat16, 8>::unpack(
+            __ldg(reinterpret_cast<const uint4*>(x + static_cast<long long>(t) * d_in + k)), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[t] = fmaf(w[e], v[e], acc[t]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TOK; ++t)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int t = 0; t < TOK; ++t) part[threadIdx.x >> 5][t] = acc[t];
+  }
+  __syncthreads();
+  if (threadIdx.x < TOK && threadIdx.x < tokens) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDownThreads / 32; ++w) sum += part[w][threadIdx.x];
+    P[static_cast<long long>(threadIdx.x) * r + blockIdx.x] = __float2bfloat16_rn(alpha * sum);
   }
 }
 
