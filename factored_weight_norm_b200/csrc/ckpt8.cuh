@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(256, 2) compose_fwd_ckpt8_kernel(
     const typename L::T* __restrict__ base, const typename L::T* __restrict__ lora,
     const typename L::T* __restrict__ bias, const float* __restrict__ m, const float* __restrict__ n, float s,
     long long tokens, long long d_out, long long blocks, typename L::T* __restrict__ y, int8_t* __restrict__ z8,
-    float* __restrict__ z_scale, long long rows_per_cta) {
+    float* __restrict__ z_scale) {
   constexpr int E = L::kE;
   const int gl = threadIdx.x % L::kLanes;
   const long long block = blockIdx.x * static_cast<long long>(blockDim.x / L::kLanes) + threadIdx.x / L::kLanes;
@@ -174,8 +174,6 @@ __global__ void __launch_bounds__(256, 2) compose_fwd_ckpt8_kernel(
     gs[e] = (mm / nn) * s;
     if (HAS_BIAS) bb[e] = ok ? ld_param(bias + col0 + c) : 0.f;
   }
-  const long long row0 = blockIdx.y * rows_per_cta;
-  const long long row1 = min(tokens, row0 + rows_per_cta);
   const int my_row = row_of_lane<L::kLanes>(gl);
   typename L::Raw rb[kCkptRows], rl[kCkptRows];
   const auto fetch = [&](long long row) {
@@ -183,16 +181,19 @@ __global__ void __launch_bounds__(256, 2) compose_fwd_ckpt8_kernel(
     for (int k = 0; k < kCkptRows; ++k) {
       rb[k] = typename L::Raw{};
       rl[k] = typename L::Raw{};
-      if (any && row + k < row1) {
+      if (any && row + k < tokens) {
         rb[k] = L::load(base + (row + k) * d_out + col0, gl, left);
         rl[k] = L::load(lora + (row + k) * d_out + col0, gl, left);
       }
     }
   };
-  fetch(row0);
-  for (long long row = row0; row < row1; row += kCkptRows) {
+  // the CTAs of a strip take groups of rows in turn, so that at any time the
+  // whole grid is on neighbouring rows
+  const long long step = static_cast<long long>(gridDim.y) * kCkptRows;
+  fetch(blockIdx.y * static_cast<long long>(kCkptRows));
+  for (long long row = blockIdx.y * static_cast<long long>(kCkptRows); row < tokens; row += step) {
     const long long at = row * d_out + col0;
-    const int rows = static_cast<int>(min(static_cast<long long>(kCkptRows), row1 - row));
+    const int rows = static_cast<int>(min(static_cast<long long>(kCkptRows), tokens - row));
     float z[kCkptRows][E];
     uint32_t tops[kCkptRows];
 #pragma unroll
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(256, 2) compose_fwd_ckpt8_kernel(
       tops[k] = any ? __float_as_uint(max_abs<E>(0.f, z[k])) : 0u;
       if (any && k < rows) L::store(y + at + k * d_out, gl, left, o);
     }
-    fetch(row + kCkptRows);  // in flight under the reduction and the codes
+    fetch(row + step);  // in flight under the reduction and the codes
     const uint32_t my_top = reduce_rows<L::kLanes>(group, gl, tops);
     const float my_inv = top_inverse(my_top);
     if ((gl & (L::kLanes / 4 - 1)) == 0 && my_row < rows) z_scale[(row + my_row) * blocks + block] = top_scale(my_top);
@@ -243,9 +244,9 @@ __global__ void __launch_bounds__(256, 2) compose_fwd_ckpt8_kernel(
 
 // ----------------------------------------------------------------- backward
 // compose_bwd_kernel's schedule (compose.cuh) with z read from the codes: a
-// CTA takes one 128-column strip of a chunk of rows, each thread carries its
-// columns' sums in fp32, and the last CTA of a strip adds the chunks' sums in
-// order.  The next rows are in flight while these are multiplied and stored.
+// CTA takes one 128-column strip of a share of the rows (a chunk: every n-th
+// group of them), each thread carries its columns' sums in fp32, and the last
+// CTA of a strip adds the chunks' sums in order.  The next rows are in flight while these are multiplied and stored.
 constexpr int kCkptBwdThreads = 256;
 constexpr int kCkptBwdRows = 4;  // rows in flight per thread
 constexpr int kCkptMaxChunks = 64;
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
     const float* __restrict__ m, const float* __restrict__ n, float s, long long tokens, long long d_out,
     long long blocks, typename L::T* __restrict__ d_base, typename L::T* __restrict__ d_lora,
     float* __restrict__ partial, unsigned long long* __restrict__ marks, float* __restrict__ d_m,
-    long long rows_per_chunk, unsigned long long tag) {
+    unsigned long long tag) {
   constexpr int E = L::kE;
   constexpr int kSlots = kCkptBwdThreads / L::kLanes;  // rows visited at once
   __shared__ float red[kSlots][kCkptBlock];
@@ -272,8 +273,10 @@ __global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
     acc[e] = 0.f;
   }
   if (L::any(gl, left)) {
-    const long long row0 = blockIdx.y * rows_per_chunk;
-    const long long row1 = min(tokens, row0 + rows_per_chunk);
+    // the CTAs of a strip take groups of rows in turn, so that at any time the
+    // whole grid is on neighbouring rows
+    const long long step = gridDim.y * static_cast<long long>(kCkptBwdRows * kSlots);
+    const long long first = blockIdx.y * static_cast<long long>(kCkptBwdRows * kSlots) + slot;
     typename L::Raw ra[kCkptBwdRows];
     typename L::Codes rz[kCkptBwdRows];
     float sc[kCkptBwdRows];
@@ -281,15 +284,15 @@ __global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
 #pragma unroll
       for (int u = 0; u < kCkptBwdRows; ++u) {
         const long long rr = row + u * kSlots;
-        if (rr < row1) {
+        if (rr < tokens) {
           ra[u] = L::load(dy + rr * d_out + col0, gl, left);
           rz[u] = L::load_codes(z8 + rr * d_out + col0, gl, left);
           sc[u] = __ldg(z_scale + rr * blocks + block);
         }
       }
     };
-    fetch(row0 + slot);
-    for (long long row = row0 + slot; row < row1; row += kCkptBwdRows * kSlots) {
+    fetch(first);
+    for (long long row = first; row < tokens; row += step) {
       typename L::Raw ca[kCkptBwdRows];
       typename L::Codes cz[kCkptBwdRows];
       float cs[kCkptBwdRows];
@@ -299,11 +302,11 @@ __global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
         cz[u] = rz[u];
         cs[u] = sc[u];
       }
-      fetch(row + kCkptBwdRows * kSlots);
+      fetch(row + step);
 #pragma unroll
       for (int u = 0; u < kCkptBwdRows; ++u) {
         const long long rr = row + u * kSlots;
-        if (rr < row1) {
+        if (rr < tokens) {
           float a[E], z[E], db[E], dl[E];
           L::unpack(ca[u], a);
           L::unpack_code(cz[u], z);

@@ -1218,16 +1218,15 @@ void launch_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const 
   const long long blocks = cdiv(d_out, kCkptBlock);
   const int threads = static_cast<int>(std::min<long long>(256, align_up(blocks * L::kLanes, 32)));
   const long long gx = cdiv(blocks, threads / L::kLanes);
-  // one wave of resident CTAs (two an SM), whole groups of rows each: a CTA
-  // starts its loads once and then keeps the next group's in flight (at 8192 x
-  // 8192 bf16 87.6 us; 90.7 with 8 CTAs an SM in turn, 103.6 with 16)
-  const long long gy = std::max<long long>(1, std::min<long long>({2LL * dev->num_sms / gx, tokens, 65535}));
-  const long long rows = align_up(cdiv(tokens, gy), kCkptRows);
+  // one wave of resident CTAs (two an SM): a CTA starts its loads once and then
+  // keeps the next group's in flight (at 8192 x 8192 bf16 87.6 us; 90.7 with 8
+  // CTAs an SM in turn, 103.6 with 16)
+  const long long gy = std::max<long long>(1, std::min<long long>({2LL * dev->num_sms / gx, cdiv(tokens, kCkptRows), 65535}));
   note_launch();
-  (bias ? compose_fwd_ckpt8_kernel<L, true> : compose_fwd_ckpt8_kernel<L, false>)<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(tokens, rows))), threads, 0,
-                                st>>>(static_cast<const T*>(base_out), static_cast<const T*>(lora_out),
-                                      static_cast<const T*>(bias), m, n, s, tokens, d_out, blocks,
-                                      static_cast<T*>(y), z8, z_scale, rows);
+  (bias ? compose_fwd_ckpt8_kernel<L, true> : compose_fwd_ckpt8_kernel<L, false>)<<<
+      dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), threads, 0, st>>>(
+      static_cast<const T*>(base_out), static_cast<const T*>(lora_out), static_cast<const T*>(bias), m, n, s, tokens,
+      d_out, blocks, static_cast<T*>(y), z8, z_scale);
 }
 
 template <typename L>
@@ -1240,14 +1239,13 @@ void launch_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_s
   // at least one row for each row of lanes
   const long long most = cdiv(tokens, kCkptBwdThreads / L::kLanes);
   const long long chunks = bwd_chunks(blocks, slots, tokens, std::min<long long>(kCkptMaxChunks, most));
-  const long long rows = cdiv(tokens, chunks);
   unsigned long long* marks = reinterpret_cast<unsigned long long*>(ws);  // tagged: no clearing needed
   float* part = reinterpret_cast<float*>(ws + blocks * kCkptMaxChunks * 8);
   note_launch();
-  compose_bwd_ckpt8_kernel<L><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(cdiv(tokens, rows))),
+  compose_bwd_ckpt8_kernel<L><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(chunks)),
                                 kCkptBwdThreads, 0, st>>>(
       static_cast<const T*>(dy), z8, z_scale, m, n, s, tokens, d_out, blocks, static_cast<T*>(d_base),
-      static_cast<T*>(d_lora), part, marks, d_m, rows, next_bwd_epoch() + 1);
+      static_cast<T*>(d_lora), part, marks, d_m, next_bwd_epoch() + 1);
 }
 
 }  // namespace

@@ -93,7 +93,7 @@ __device__ __forceinline__ void slice_join(const SliceArgs& a, uint32_t area, co
     ld_shared8(rowf + kLinBM + group, g);
     ld_shared8(rowf + 2 * kLinBM + group, b);
   }
-#pragma unroll 1
+#pragma unroll (S == 1 ? 4 : 1)
   for (int j = (threadIdx.x >> 4) * S + static_cast<int>(rank); j < BN; j += (kSlThreads / 16) * S) {
     const int t = tok0 + j;
     if (t >= a.tokens) break;
