@@ -962,6 +962,7 @@ int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const 
                  cudaStream_t st) {
   const int bn = slice_bn(a.tokens);
   const long long row_tiles = cdiv(a.rows, kLinBM), tok_tiles = cdiv(a.tokens, bn);
+  if (row_tiles * tok_tiles > INT32_MAX / 8) return DORA_ERR_UNSUPPORTED;
   const bool one = (i8 && bn > 64) || room > 0;  // a CTA an SM
   if (room == 0) room = (one ? 1LL : 2LL) * dev->num_sms;
   int splits = 1;
@@ -983,7 +984,7 @@ int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const 
   cfg.numAttrs = after ? 2 : 1;
   cfg.blockDim = dim3(kSlThreads);
   cfg.dynamicSmemBytes = smem;
-  cfg.gridDim = dim3(static_cast<unsigned>(row_tiles * splits), static_cast<unsigned>(tok_tiles));
+  cfg.gridDim = dim3(static_cast<unsigned>(row_tiles * tok_tiles * splits));
   note_launch();
   return cudaLaunchKernelEx(&cfg, slice_kernel(i8, bn), tmW, tmX, tmB, tmP, a) == cudaSuccess ? DORA_OK
                                                                                                : DORA_ERR_CUDA;

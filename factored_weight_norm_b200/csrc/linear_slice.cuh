@@ -235,8 +235,10 @@ __global__ void __launch_bounds__(kSlThreads)
   uint32_t splits;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
   const uint32_t rank = cluster_ctarank();
-  const int row0 = static_cast<int>(blockIdx.x / splits) * kLinBM;
-  const int tok0 = static_cast<int>(blockIdx.y) * BN;
+  // clusters along x: all row tiles of a token tile, then the next token tile
+  const unsigned tile = blockIdx.x / splits, row_tiles = (a.rows + kLinBM - 1) / kLinBM;
+  const int row0 = static_cast<int>(tile % row_tiles) * kLinBM;
+  const int tok0 = static_cast<int>(tile / row_tiles) * BN;
   const int kb0 = slice_start(a, static_cast<int>(rank), static_cast<int>(splits));
   const int kb1 = slice_start(a, static_cast<int>(rank) + 1, static_cast<int>(splits));
   const bool has_ext = I8 && kb1 > a.kb_main;

@@ -470,6 +470,9 @@ def dora_fused_linear_fwd_ckpt8(x, W, A, B, m, n, s: float, bias=None, y=None, z
 
     z8 are int8 codes [tokens, d_out], z_scale their fp32 scales for every 128
     columns of a token; ``dora_compose_bwd_ckpt8`` reads them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dora_fused_linear_fwd_ckpt8(x, W, A, B, m, n, s, bias, y, z8, z_scale, workspace)
     where = "dora_fused_linear_fwd_ckpt8"
     if x.dim() != 2 or W.dim() != 2:
         raise ValueError(f"{where}: x, W, A and B must be 2-D")
@@ -547,6 +550,10 @@ def dora_factored_norm_bwd(W, A, B, s: float, n, d_n, dA=None, dB=None, workspac
 
 
 # ---------------------------------------------------------- 8-bit operators
+# A call given a stream runs with that stream current, so that the outputs and
+# workspaces it makes belong to that stream too: one made on the current stream
+# could be memory that the current stream still uses, and be handed out again
+# there while the other stream still works on it.
 def _typed(where: str, name: str, t, shape, dtype):
     """t (None skipped) has this shape and dtype."""
     if t is None or (t.dtype is dtype and t.shape == shape):
@@ -598,10 +605,13 @@ def dora_quantize_rows_i8(x, residual=None, h=None, q=None, scale=None, stream=N
 
     h is written in x's type where there is a residual (it may be x or
     residual itself) and None without one (the codes are x's)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dora_quantize_rows_i8(x, residual, h, q, scale)
     where = "dora_quantize_rows_i8"
     rows, cols, dt, h, q, scale = _rows_i8(where, x, residual, None, h, None, q, scale)
     _check(lib().dora_quantize_rows_i8(_ptr(x), _ptr(residual), rows, cols, dt, _ptr(h), _ptr(q), _ptr(scale),
-                                       _stream(stream)), where)
+                                       _stream()), where)
     return q, scale, h
 
 
@@ -611,6 +621,9 @@ def dora_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, want_y: bool =
 
     h as in dora_quantize_rows_i8; y is the norm in x's type (the adapter
     branch's input), None unless it is passed or ``want_y`` is true."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dora_rms_norm_i8(x, weight, eps, residual, want_y, h, y, q, scale)
     where = "dora_rms_norm_i8"
     if weight is None:
         raise ValueError(f"{where}: a weight is required")
@@ -618,12 +631,15 @@ def dora_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, want_y: bool =
     if y is None and want_y:
         y = torch.empty_like(x)
     _check(lib().dora_rms_norm_i8(_ptr(x), _ptr(residual), _ptr(weight), eps, rows, cols, dt, _ptr(h), _ptr(y),
-                                  _ptr(q), _ptr(scale), _stream(stream)), where)
+                                  _ptr(q), _ptr(scale), _stream()), where)
     return q, scale, h, y
 
 
 def dora_dequantize_i8(q, scale, dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
     """q * scale in ``dtype``; scale is [rows], or [rows, ceil(cols / 128)] as a checkpoint's."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dora_dequantize_i8(q, scale, dtype, out)
     where = "dora_dequantize_i8"
     if q.dim() != 2:
         raise ValueError(f"{where}: q must be 2-D [rows, cols], got {tuple(q.shape)}")
@@ -640,7 +656,7 @@ def dora_dequantize_i8(q, scale, dtype: torch.dtype = torch.bfloat16, out=None, 
     _dense_cuda(q, scale, out)
     if out is None:
         out = torch.empty_like(q, dtype=dtype)
-    _check(lib().dora_dequantize_i8(_ptr(q), _ptr(scale), rows, cols, block, dt, _ptr(out), _stream(stream)), where)
+    _check(lib().dora_dequantize_i8(_ptr(q), _ptr(scale), rows, cols, block, dt, _ptr(out), _stream()), where)
     return out
 
 
@@ -654,6 +670,9 @@ def dora_linear_i8_fwd(x_q, x_scale, W_q, w_scale, x=None, A=None, B=None, m=Non
 
     x, A and B (bf16) are the adapter's branch, all given or all None; m and n
     both None is m / n = 1."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dora_linear_i8_fwd(x_q, x_scale, W_q, w_scale, x, A, B, m, n, s, bias, y, workspace)
     where = "dora_linear_i8_fwd"
     if x_q.dim() != 2 or W_q.dim() != 2:
         raise ValueError(f"{where}: x_q and W_q must be 2-D")
@@ -686,7 +705,7 @@ def dora_linear_i8_fwd(x_q, x_scale, W_q, w_scale, x=None, A=None, B=None, m=Non
     st = lib().dora_linear_i8_fwd(
         _ptr(x_q), _ptr(x_scale), _ptr(W_q), _ptr(w_scale), _ptr(x), _ptr(A), _ptr(B), _ptr(bias), _ptr(m), _ptr(n),
         float(s), T, d_in, d_out, r, DORA_BF16, _ptr(y), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(),
     )
     _check(st, where)
     return y
@@ -697,6 +716,9 @@ def dora_compose_fwd_ckpt8(base_out, lora_out, m, n, s: float, y=None, z8=None, 
 
     z8 are int8 codes [tokens, d_out], z_scale their fp32 scales for every 128
     columns of a token; ``dora_compose_bwd_ckpt8`` reads them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dora_compose_fwd_ckpt8(base_out, lora_out, m, n, s, y, z8, z_scale, bias=bias)
     where = "dora_compose_fwd_ckpt8"
     _acts2d(base_out, where)
     tokens, d_out = base_out.shape
@@ -709,7 +731,7 @@ def dora_compose_fwd_ckpt8(base_out, lora_out, m, n, s: float, y=None, z8=None, 
         y = torch.empty_like(base_out)
     st = lib().dora_compose_fwd_ckpt8(
         _ptr(base_out), _ptr(lora_out), _ptr(bias), _ptr(m), _ptr(n), float(s), tokens, d_out, _dt(base_out), _ptr(y),
-        _ptr(z8), _ptr(z_scale), _stream(stream),
+        _ptr(z8), _ptr(z_scale), _stream(),
     )
     _check(st, where)
     return y, z8, z_scale
@@ -722,6 +744,9 @@ def dora_compose_bwd_ckpt8_workspace_size(tokens: int, d_out: int) -> int:
 def dora_compose_bwd_ckpt8(dy, z8, z_scale, m, n, s: float, d_base=None, d_lora=None, d_m=None, workspace=None,
                            stream=None):
     """(d_base, d_lora, d_m) of the compose from its 8-bit checkpoint, with n held constant and the bias frozen."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dora_compose_bwd_ckpt8(dy, z8, z_scale, m, n, s, d_base, d_lora, d_m, workspace)
     where = "dora_compose_bwd_ckpt8"
     _acts2d(dy, where)
     tokens, d_out = dy.shape
@@ -741,7 +766,7 @@ def dora_compose_bwd_ckpt8(dy, z8, z_scale, m, n, s: float, d_base=None, d_lora=
                                 device=dy.device)
     st = lib().dora_compose_bwd_ckpt8(
         _ptr(dy), _ptr(z8), _ptr(z_scale), _ptr(m), _ptr(n), float(s), tokens, d_out, _dt(dy), _ptr(d_base),
-        _ptr(d_lora), _ptr(d_m), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream),
+        _ptr(d_lora), _ptr(d_m), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(),
     )
     _check(st, where)
     return d_base, d_lora, d_m

@@ -290,3 +290,16 @@ def test_fused_scales_hold_fp32_over_a_long_k():
     top = np.stack([np.max(np.abs(z[:, j:j + 128]), axis=1) for j in range(0, N, 128)], axis=1)
     rel = np.linalg.norm(127 * zs.cpu().double().numpy() - top) / np.linalg.norm(top)
     assert rel <= 64 * 2.0 ** -23, rel
+
+
+def test_a_given_stream_runs_the_training_pair():
+    base, lora, m, n, _, dy = _acts(70, 1000, BF, False, seed=13)
+    ref = D.dora_compose_fwd_ckpt8(base, lora, m, n, 0.5)
+    back = D.dora_compose_bwd_ckpt8(dy, ref[1], ref[2], m, n, 0.5)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = D.dora_compose_fwd_ckpt8(base, lora, m, n, 0.5, stream=side)
+        gb = D.dora_compose_bwd_ckpt8(dy, got[1], got[2], m, n, 0.5, stream=side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*got, *gb), (*ref, *back)))

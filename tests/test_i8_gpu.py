@@ -360,3 +360,41 @@ def test_linear_i8_headline_sampled():
     torch.cuda.synchronize()
     assert D.dora_device_status() == D.DORA_OK
     _check_linear(k, y, rows=np.array([0, 127, 128, 255, 256, 4099, 8191]), cols=np.array([0, 127, 128, 300, 8191]))
+
+
+def test_a_given_stream_owns_what_the_call_makes():
+    # memory freed behind long work on the current stream must not become the
+    # output of a call on another one, nor that call's workspace go back early
+    k = _module(40, 2048, 1024, 64, seed=61)
+    ref = D.dora_linear_i8_fwd(**k)
+    x = _rows(40, 2048, BF, 62)
+    q0, s0, _ = D.dora_quantize_rows_i8(x)
+    v0 = D.dora_dequantize_i8(q0, s0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = torch.randn(4096, 4096, device=DEV)
+    for _ in range(5):
+        for n in (ref.numel(), q0.numel() // 2, 40 * 64, 256):
+            t = torch.zeros(n, dtype=BF, device=DEV)
+            for _ in range(4):
+                busy = busy @ busy * 1e-3
+            t.add_(busy.flatten()[: n].to(BF))  # late on the current stream
+            del t
+        y = D.dora_linear_i8_fwd(**k, stream=side)
+        q, sc, _ = D.dora_quantize_rows_i8(x, stream=side)
+        v = D.dora_dequantize_i8(q, sc, stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref) and torch.equal(q, q0) and torch.equal(sc, s0) and torch.equal(v, v0)
+
+
+def test_linear_i8_of_millions_of_tokens():
+    # more token tiles than one grid dimension but the first holds
+    T = 8_400_003
+    k = _module(T, 16, 8, 8, seed=63)
+    y = D.dora_linear_i8_fwd(**k)
+    torch.cuda.synchronize()
+    assert D.dora_device_status() == D.DORA_OK
+    rows = np.array([0, 1, 127, 255, 4_000_000, 8_388_607, 8_388_608, T - 1])
+    small = {n: (k[n] if n not in ("x_q", "x_scale", "x") else k[n][torch.as_tensor(rows, device=DEV)]) for n in k}
+    _check_linear(small, y[torch.as_tensor(rows, device=DEV)])
