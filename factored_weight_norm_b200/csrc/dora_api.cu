@@ -1021,6 +1021,15 @@ int launch_p_slice(const void* x, const void* A, __nv_bfloat16* P, __nv_bfloat16
   return launch_slice(false, tmA, tmX, tmA, tmX, sa, false, beside ? spare : 0, dev, st);
 }
 
+// Tile width of the products with whole accumulators in registers: 128-wide
+// tiles take about 0.58 of a 256-wide one's time (256 tokens through 8192 x 8192
+// in 8 bits: 26 us, 31 on 256-wide tiles that fill 32 of 74 pairs), so the width
+// whose waves over the pairs end first.
+int pick_bn_waves(long long tiles_m, long long N, const DeviceInfo* dev) {
+  const auto waves = [&](int width) { return cdiv(tiles_m * cdiv(N, width), dev->pair_clusters); };
+  return 58 * waves(128) < 100 * waves(256) ? 128 : 256;
+}
+
 int fused_linear(const void* x, const void* W, const void* A, const void* B, const void* bias, const float* m,
                  const float* n, float s, int64_t tokens, int64_t d_in, int64_t d_out, int64_t r, dora_dtype dt,
                  void* y, bool ckpt, int8_t* z8, float* z_scale, void* workspace, size_t workspace_bytes,
@@ -1047,7 +1056,7 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
   __nv_bfloat16* P = static_cast<__nv_bfloat16*>(workspace);
 
   // B-side boxes hold the bn / 2 rows one CTA of a pair owns
-  const int bn_p = r > 0 ? pick_bn(r) : 256, bn_y = ckpt ? kPairBN : pick_bn(d_out);
+  const int bn_p = r > 0 ? pick_bn(r) : 256, bn_y = ckpt ? pick_bn_waves(cdiv(tokens, kPairBM), d_out, dev) : pick_bn(d_out);
   CUtensorMap tmX, tmW, tmA, tmP, tmB;
   if (make_map(&tmX, x, tokens, d_in) || make_map(&tmW, W, d_out, d_in, bn_y / 2)) return DORA_ERR_CUDA;
   if (r > 0 && (make_map(&tmA, A, r, d_in, bn_p / 2) || make_map(&tmP, P, tokens, r) ||
@@ -1060,7 +1069,7 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
   cudaLaunchAttribute attrs[2];
   if (ckpt) {
     __nv_bfloat16* P_lo = r > 0 ? P + p_bytes / 2 : nullptr;
-    if (r > 0 && launch_p_slice(x, A, P, P_lo, s, tokens, d_in, r, tiles_m2 * cdiv(d_out, kPairBN), dev, st))
+    if (r > 0 && launch_p_slice(x, A, P, P_lo, s, tokens, d_in, r, tiles_m2 * cdiv(d_out, bn_y), dev, st))
       return DORA_ERR_CUDA;
     CUtensorMap tmLo;
     if (r > 0 && make_map(&tmLo, P_lo, tokens, r)) return DORA_ERR_CUDA;
@@ -1070,7 +1079,8 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
     ca.kb_main = kb_main;
     ca.kb_r = static_cast<int>(cdiv(r, kLinBK));
     ca.tiles_m = static_cast<int>(tiles_m2);
-    ca.tiles_n = static_cast<int>(cdiv(d_out, kPairBN));
+    ca.tiles_n = static_cast<int>(cdiv(d_out, bn_y));
+    ca.bn = bn_y;
     ca.stages = linear_i8_stages(dev->smem_optin);
     ca.m = m;
     ca.n = n;
@@ -1357,11 +1367,8 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
     sa.out = static_cast<__nv_bfloat16*>(y);
     return launch_slice(true, tmWq, tmXq, r > 0 ? tmB : tmWq, r > 0 ? tmP : tmXq, sa, r > 0, 0, dev, st);
   }
-  // 128-wide tiles take 0.58 of a 256-wide one's time: the width whose waves over
-  // the pairs end first
   const long long tiles_m = cdiv(tokens, kPairBM);
-  const auto waves = [&](int width) { return cdiv(tiles_m * cdiv(d_out, width), dev->pair_clusters); };
-  const int bn = 58 * waves(128) < 100 * waves(256) ? 128 : 256;
+  const int bn = pick_bn_waves(tiles_m, d_out, dev);
   if (make_map_i8(&tmXq, x_q, tokens, d_in, kLinBM) || make_map_i8(&tmWq, W_q, d_out, d_in, bn / 2)) return DORA_ERR_CUDA;
   if (r > 0 && (make_map(&tmP, P, tokens, r) || make_map(&tmB, B, d_out, r, bn / 2) ||
                 launch_p_slice(x, A, P, nullptr, s, tokens, d_in, r, tiles_m * cdiv(d_out, bn), dev, st)))

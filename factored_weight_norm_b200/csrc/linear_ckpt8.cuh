@@ -17,7 +17,9 @@
 // thread's 128 columns of its row are one stretch, so the maximum and the
 // codes come from registers without any exchange.  Two TMEM accumulators: the
 // tensor core sums one chunk while the warps fetch the other, and a tile's
-// last step overlaps the next tile's first two chunks.
+// last step overlaps the next tile's first two chunks.  Tiles of 128 columns
+// (four of the warps then only keep step) serve products whose 256-wide tiles
+// leave half of the pairs without one.
 #pragma once
 
 #include "linear_i8.cuh"
@@ -31,6 +33,7 @@ struct LinearCkptArgs {
   int M, N;
   int kb_main, kb_r;      // K blocks of x W^T and of each half of P B^T
   int tiles_m, tiles_n;
+  int bn;                 // pair tile width along N: 256 or 128
   int stages;
   const float* m;
   const float* n;
@@ -70,6 +73,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int kb_total = a.kb_main + 2 * a.kb_r;
   const int n_stages = (kb_total + kPairKps - 1) / kPairKps;  // per tile
   const int n_chunks = (n_stages + kCkChunk - 1) / kCkChunk;  // chunk c ends before stage n_stages (c + 1) / n_chunks
+
+  // bytes that both CTAs' copies bring per stage
+  const uint32_t stage_tx = 2 * kPairKps * (kLinABytes + a.bn / 2 * 128u);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
@@ -116,7 +122,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         int tm, tn;
         lin_tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
         const int yx = tm * kPairBM + static_cast<int>(rank) * kLinBM;
-        const int yw = tn * kPairBN + static_cast<int>(rank) * (kPairBN / 2);
+        const int yw = tn * a.bn + static_cast<int>(rank) * (a.bn / 2);
         for (int kb0 = 0; kb0 < kb_total; kb0 += kPairKps) {
           if (kb0 + kPairKps > a.kb_main && !ext_ready) {
             grid_dep_wait();  // P comes from the launch before
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           bool got = true;
           if (lane == 0) {
             got = mbar_wait(&empty[stage], phase ^ 1u, limit);
-            if (got && leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStageBytes);
+            if (got && leader) mbar_arrive_expect_tx(&full[stage], stage_tx);
             if (!got) lin_timeout(a.status, abort_flag);
           }
           got = __shfl_sync(0xffffffffu, got, 0);
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t idesc = idesc_bf16_f32(kPairBM, kPairBN);
+        const uint32_t idesc = idesc_bf16_f32(kPairBM, a.bn);
         const uint64_t desc0 = sw128_kmajor_desc(base_s);
         const uint64_t desc_step = kPairStageBytes >> 4;
         uint32_t it = 0;  // chunks so far
@@ -213,6 +219,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     const int half = (warp - 4) >> 2;  // columns half * 128 .. of the tile
+    const bool mine = half * 128 < a.bn;
     const int et = threadIdx.x - 128;
     const uint32_t tmem_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
@@ -226,9 +233,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       // read by warps finishing the tile before
       float* cf = cols + (tile & 1u) * 3 * kPairBN;
       {
-        const int c = tn * kPairBN + et;
+        const int c = tn * a.bn + et;
         float g = 0.f, b = 0.f;
-        if (c < a.N) {
+        if (et < a.bn && c < a.N) {
           g = __ldg(a.m + c) / __ldg(a.n + c);
           if (a.bias) b = __bfloat162float(a.bias[c]);
         }
@@ -248,21 +255,23 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         }
         if (!alive) continue;
         tc_fence_after();
+        if (mine) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t u[16];
-          tmem_ld16(tmem_lane + ab * kPairBN + j * 16, u);
+          for (int j = 0; j < 8; ++j) {
+            uint32_t u[16];
+            tmem_ld16(tmem_lane + ab * kPairBN + j * 16, u);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[j * 16 + e] += __uint_as_float(u[e]);
+            for (int e = 0; e < 16; ++e) v[j * 16 + e] += __uint_as_float(u[e]);
+          }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(acc_empty_leader + ab * 8u);
       }
       const long long row = static_cast<long long>(tm) * kPairBM + rank * kLinBM + q * 32 + lane;
-      const int col0 = tn * kPairBN + half * 128;
+      const int col0 = tn * a.bn + half * 128;
       uint32_t open = 0;  // groups of eight codes that fp32 leaves open
-      if (alive && col0 < a.N) {  // warp-uniform
+      if (alive && mine && col0 < a.N) {  // warp-uniform
         // columns past N are sums of zero-filled operands: they do not count
         const uint32_t top = __float_as_uint(max_abs<128>(0.f, v));
         const float inv = top_inverse(top);
