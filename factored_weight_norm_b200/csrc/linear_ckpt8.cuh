@@ -11,7 +11,7 @@
 //  * The tensor core drops the bits below its accumulator as it adds, always
 //    toward zero: over K = 8192 that took 8.5e-6 of the largest values
 //    (4.0e-6 at 4096).  So K is cut into chunks of at most kCkChunk stages
-//    (1024 of K), each summed in TMEM from zero, and the epilogue warps add
+//    (768 of K), each summed in TMEM from zero, and the epilogue warps add
 //    the chunks in fp32 registers, which round to nearest.
 // Eight epilogue warps hold a 128 x 256 tile in 128 registers a thread; a
 // thread's 128 columns of its row are one stretch, so the maximum and the

@@ -156,7 +156,9 @@ def test_outputs_stay_inside_their_rows():
 
 
 FUSED = [(128, 64, 256, 16), (300, 520, 1000, 48), (257, 1024, 512, 384), (64, 4104, 264, 512), (1, 64, 8, 8),
-         (130, 136, 2056, 40), (96, 128, 120, 0), (200, 256, 128, 8), (520, 264, 392, 24)]
+         (130, 136, 2056, 40), (96, 128, 120, 0), (200, 256, 128, 8), (520, 264, 392, 24),
+         (140, 8, 136, 256),                        # more rank than input columns
+         (2560, 64, 3840, 8), (2500, 64, 5000, 24)]  # several waves of 128- and of 256-wide tiles
 
 
 @pytest.mark.parametrize("T, d_in, d_out, r", FUSED)
@@ -273,10 +275,9 @@ def test_offsets_past_32_bits():
 
 
 def test_fused_scales_hold_fp32_over_a_long_k():
-    # the scales of z at K = 8192: an fp32 sum that rounds to nearest every 1024
-    # terms.  Within a chunk the tensor core's additions (of 16 products) drop
-    # bits, at most 2^-23 of the running sum each: 64 of them, and the running
-    # sum of a row that ends at its maximum is at most that of the magnitudes
+    # the scales of z at K = 8192: an fp32 sum of chunks of at most 1024 terms.
+    # Within a chunk the tensor core's additions (of 16 products) drop bits, at
+    # most 2^-23 of the running sum each: 64 of them
     T, K, N, r = 130, 8192, 384, 64
     g = _gen(12)
     x = torch.randn(T, K, generator=g).to(BF).to(DEV)

@@ -204,7 +204,10 @@ def _check_linear(k, y, rows=slice(None), cols=slice(None)):
 LINEAR = [(1, 16, 8, 8), (1, 8192, 264, 384), (2, 144, 136, 0), (7, 1040, 1000, 48), (16, 528, 520, 64),
           (17, 4112, 256, 16), (33, 2048, 4096, 384), (64, 272, 392, 72), (65, 512, 128, 8), (128, 1024, 2056, 0),
           (129, 400, 264, 40), (200, 2064, 1000, 128), (256, 256, 2048, 64), (300, 640, 512, 384), (513, 1024, 776, 8),
-          (1030, 528, 264, 24)]
+          (1030, 528, 264, 24),
+          (5, 16, 24, 512), (300, 32, 264, 1000),  # more rank than input columns
+          (2560, 64, 3840, 8),                     # several waves of 128-wide tiles
+          (2500, 64, 5000, 24)]                    # several waves of 256-wide ones
 
 
 @pytest.mark.parametrize("T, d_in, d_out, r", LINEAR)
