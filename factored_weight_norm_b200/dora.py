@@ -210,11 +210,12 @@ def _dense_cuda(*ts):
             if dev < 0:
                 raise ValueError("tensors must live on a CUDA device")
             if cur is None:
-                cur = torch.cuda.current_device()
+                cur = torch._C._cuda_getDevice()  # CUDA is up: a tensor lives there
             if dev != cur:
                 raise ValueError(f"tensor on {t.device} but the current device is cuda:{cur}")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous (row-major)")
+    return cur
 
 
 def _like(ref, where: str, **named):
@@ -554,9 +555,16 @@ def dora_factored_norm_bwd(W, A, B, s: float, n, d_n, dA=None, dB=None, workspac
 # workspaces it makes belong to that stream too: one made on the current stream
 # could be memory that the current stream still uses, and be handed out again
 # there while the other stream still works on it.
+#
+# A small call costs the host more than the GPU, so the checks below compare in
+# place and go to _typed only to say what is wrong, and the stream comes from
+# the device that _dense_cuda has just found.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # None in a build without CUDA
+
+
 def _typed(where: str, name: str, t, shape, dtype):
     """t (None skipped) has this shape and dtype."""
-    if t is None or (t.dtype is dtype and t.shape == shape):
+    if t is None:
         return
     if t.shape != shape:
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -570,34 +578,42 @@ def _checkpoint(where, tokens, d_out, z8, z_scale, device):
     _typed(where, "z8", z8, (tokens, d_out), torch.int8)
     _typed(where, "z_scale", z_scale, (tokens, blocks), torch.float32)
     if z8 is None:
-        z8 = torch.empty(tokens, d_out, dtype=torch.int8, device=device)
+        z8 = torch.empty((tokens, d_out), dtype=torch.int8, device=device)
     if z_scale is None:
-        z_scale = torch.empty(tokens, blocks, dtype=torch.float32, device=device)
+        z_scale = torch.empty((tokens, blocks), dtype=torch.float32, device=device)
     return z8, z_scale
 
 
 def _rows_i8(where, x, residual, weight, h, y, q, scale):
-    """Checks the rows' operands and makes the outputs that are not given: (rows, cols, dt, h, q, scale)."""
+    """Checks the rows' operands and makes the outputs that are not given:
+    (rows, cols, dt, h, q, scale, stream)."""
     if x.dim() != 2:
         raise ValueError(f"{where}: activations must be 2-D [tokens, d_out], got {tuple(x.shape)}")
     dt, shape, dtype = _dt(x), x.shape, x.dtype
     rows, cols = shape
-    _typed(where, "residual", residual, shape, dtype)
-    _typed(where, "h", h, shape, dtype)
-    _typed(where, "y", y, shape, dtype)
-    _typed(where, "weight", weight, (cols,), dtype)
-    _typed(where, "q", q, shape, torch.int8)
-    _typed(where, "scale", scale, (rows,), torch.float32)
-    if h is not None and residual is None:
+    if residual is not None:
+        if residual.dtype is not dtype or residual.shape != shape:
+            _typed(where, "residual", residual, shape, dtype)
+    elif h is not None:
         raise ValueError(f"{where}: h is x + residual, so it needs a residual")
-    _dense_cuda(x, residual, weight, h, y, q, scale)
+    if weight is not None and (weight.dtype is not dtype or weight.shape != (cols,)):
+        _typed(where, "weight", weight, (cols,), dtype)
+    if h is not None:
+        _typed(where, "h", h, shape, dtype)
+    if y is not None:
+        _typed(where, "y", y, shape, dtype)
+    if q is not None:
+        _typed(where, "q", q, shape, torch.int8)
+    if scale is not None:
+        _typed(where, "scale", scale, (rows,), torch.float32)
+    dev = _dense_cuda(x, residual, weight, h, y, q, scale)
     if residual is not None and h is None:
         h = torch.empty_like(x)
     if q is None:
         q = torch.empty_like(x, dtype=torch.int8)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    return rows, cols, dt, h, q, scale
+        scale = x.new_empty(rows, dtype=torch.float32)
+    return rows, cols, dt, h, q, scale, _raw_stream(dev)
 
 
 def dora_quantize_rows_i8(x, residual=None, h=None, q=None, scale=None, stream=None):
@@ -609,9 +625,9 @@ def dora_quantize_rows_i8(x, residual=None, h=None, q=None, scale=None, stream=N
         with torch.cuda.stream(stream):
             return dora_quantize_rows_i8(x, residual, h, q, scale)
     where = "dora_quantize_rows_i8"
-    rows, cols, dt, h, q, scale = _rows_i8(where, x, residual, None, h, None, q, scale)
-    _check(lib().dora_quantize_rows_i8(_ptr(x), _ptr(residual), rows, cols, dt, _ptr(h), _ptr(q), _ptr(scale),
-                                       _stream()), where)
+    rows, cols, dt, h, q, scale, st = _rows_i8(where, x, residual, None, h, None, q, scale)
+    _check(lib().dora_quantize_rows_i8(x.data_ptr(), _ptr(residual), rows, cols, dt, _ptr(h), q.data_ptr(),
+                                       scale.data_ptr(), st), where)
     return q, scale, h
 
 
@@ -627,11 +643,11 @@ def dora_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, want_y: bool =
     where = "dora_rms_norm_i8"
     if weight is None:
         raise ValueError(f"{where}: a weight is required")
-    rows, cols, dt, h, q, scale = _rows_i8(where, x, residual, weight, h, y, q, scale)
+    rows, cols, dt, h, q, scale, st = _rows_i8(where, x, residual, weight, h, y, q, scale)
     if y is None and want_y:
         y = torch.empty_like(x)
-    _check(lib().dora_rms_norm_i8(_ptr(x), _ptr(residual), _ptr(weight), eps, rows, cols, dt, _ptr(h), _ptr(y),
-                                  _ptr(q), _ptr(scale), _stream()), where)
+    _check(lib().dora_rms_norm_i8(x.data_ptr(), _ptr(residual), weight.data_ptr(), eps, rows, cols, dt, _ptr(h),
+                                  _ptr(y), q.data_ptr(), scale.data_ptr(), st), where)
     return q, scale, h, y
 
 
@@ -643,20 +659,26 @@ def dora_dequantize_i8(q, scale, dtype: torch.dtype = torch.bfloat16, out=None, 
     where = "dora_dequantize_i8"
     if q.dim() != 2:
         raise ValueError(f"{where}: q must be 2-D [rows, cols], got {tuple(q.shape)}")
-    rows, cols = q.shape
-    block = 0 if scale.dim() == 1 else CKPT_BLOCK
-    _typed(where, "q", q, q.shape, torch.int8)
-    _typed(where, "scale", scale, (rows,) if block == 0 else (rows, -(-cols // CKPT_BLOCK)), torch.float32)
+    shape = q.shape
+    rows, cols = shape
+    if scale.dim() == 1:
+        block, scales = 0, (rows,)
+    else:
+        block, scales = CKPT_BLOCK, (rows, -(-cols // CKPT_BLOCK))
+    if q.dtype is not torch.int8 or scale.dtype is not torch.float32 or scale.shape != scales:
+        _typed(where, "q", q, shape, torch.int8)
+        _typed(where, "scale", scale, scales, torch.float32)
     if out is not None:
         dtype = out.dtype
-        _typed(where, "out", out, q.shape, dtype)
+        _typed(where, "out", out, shape, dtype)
     dt = DORA_BF16 if dtype is torch.bfloat16 else DORA_F32
     if dt == DORA_F32 and dtype is not torch.float32:
         raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32 only")
-    _dense_cuda(q, scale, out)
+    dev = _dense_cuda(q, scale, out)
     if out is None:
         out = torch.empty_like(q, dtype=dtype)
-    _check(lib().dora_dequantize_i8(_ptr(q), _ptr(scale), rows, cols, block, dt, _ptr(out), _stream()), where)
+    _check(lib().dora_dequantize_i8(q.data_ptr(), scale.data_ptr(), rows, cols, block, dt, out.data_ptr(),
+                                    _raw_stream(dev)), where)
     return out
 
 
@@ -678,34 +700,43 @@ def dora_linear_i8_fwd(x_q, x_scale, W_q, w_scale, x=None, A=None, B=None, m=Non
         raise ValueError(f"{where}: x_q and W_q must be 2-D")
     T, d_in = x_q.shape
     d_out = W_q.shape[0]
-    _typed(where, "x_q", x_q, (T, d_in), torch.int8)
-    _typed(where, "W_q", W_q, (d_out, d_in), torch.int8)
-    _typed(where, "x_scale", x_scale, (T,), torch.float32)
-    _typed(where, "w_scale", w_scale, (d_out,), torch.float32)
-    if len({x is None, A is None, B is None}) != 1:
-        raise ValueError(f"{where}: x, A and B come together")
-    if (m is None) != (n is None):
-        raise ValueError(f"{where}: m and n come together")
+    i8, bf16, f32 = torch.int8, torch.bfloat16, torch.float32
+    if x_q.dtype is not i8 or W_q.dtype is not i8 or W_q.shape != (d_out, d_in):
+        _typed(where, "x_q", x_q, (T, d_in), i8)
+        _typed(where, "W_q", W_q, (d_out, d_in), i8)
+    if x_scale.dtype is not f32 or w_scale.dtype is not f32 or x_scale.shape != (T,) or w_scale.shape != (d_out,):
+        _typed(where, "x_scale", x_scale, (T,), f32)
+        _typed(where, "w_scale", w_scale, (d_out,), f32)
     r = 0
-    if A is not None:
+    if A is not None and x is not None and B is not None:
         if A.dim() != 2:
             raise ValueError(f"{where}: A must be 2-D")
         r = A.shape[0]
-        _typed(where, "x", x, (T, d_in), torch.bfloat16)
-        _typed(where, "A", A, (r, d_in), torch.bfloat16)
-        _typed(where, "B", B, (d_out, r), torch.bfloat16)
-    _vec_f32(d_out, where, m=m, n=n)
-    _typed(where, "bias", bias, (d_out,), torch.bfloat16)
-    _typed(where, "y", y, (T, d_out), torch.bfloat16)
-    _dense_cuda(x_q, x_scale, W_q, w_scale, x, A, B, m, n, bias, y, workspace)
+        if (x.dtype is not bf16 or A.dtype is not bf16 or B.dtype is not bf16 or x.shape != (T, d_in)
+                or A.shape != (r, d_in) or B.shape != (d_out, r)):
+            _typed(where, "x", x, (T, d_in), bf16)
+            _typed(where, "A", A, (r, d_in), bf16)
+            _typed(where, "B", B, (d_out, r), bf16)
+    elif A is not None or x is not None or B is not None:
+        raise ValueError(f"{where}: x, A and B come together")
+    if m is not None and n is not None:
+        if m.dtype is not f32 or n.dtype is not f32 or m.shape != (d_out,) or n.shape != (d_out,):
+            _vec_f32(d_out, where, m=m, n=n)
+    elif m is not None or n is not None:
+        raise ValueError(f"{where}: m and n come together")
+    if bias is not None:
+        _typed(where, "bias", bias, (d_out,), bf16)
+    if y is not None:
+        _typed(where, "y", y, (T, d_out), bf16)
+    dev = _dense_cuda(x_q, x_scale, W_q, w_scale, x, A, B, m, n, bias, y, workspace)
     if y is None:
-        y = torch.empty(T, d_out, dtype=torch.bfloat16, device=x_q.device)
+        y = x_q.new_empty((T, d_out), dtype=bf16)
     if workspace is None and r > 0:
-        workspace = torch.empty(dora_linear_i8_fwd_workspace_size(T, r), dtype=torch.uint8, device=x_q.device)
+        workspace = x_q.new_empty(lib().dora_linear_i8_fwd_workspace_size(T, r), dtype=torch.uint8)
     st = lib().dora_linear_i8_fwd(
-        _ptr(x_q), _ptr(x_scale), _ptr(W_q), _ptr(w_scale), _ptr(x), _ptr(A), _ptr(B), _ptr(bias), _ptr(m), _ptr(n),
-        float(s), T, d_in, d_out, r, DORA_BF16, _ptr(y), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(),
+        x_q.data_ptr(), x_scale.data_ptr(), W_q.data_ptr(), w_scale.data_ptr(), _ptr(x), _ptr(A), _ptr(B), _ptr(bias),
+        _ptr(m), _ptr(n), s, T, d_in, d_out, r, DORA_BF16, y.data_ptr(), _ptr(workspace),
+        0 if workspace is None else workspace.nbytes, _raw_stream(dev),
     )
     _check(st, where)
     return y
@@ -720,18 +751,31 @@ def dora_compose_fwd_ckpt8(base_out, lora_out, m, n, s: float, y=None, z8=None, 
         with torch.cuda.stream(stream):
             return dora_compose_fwd_ckpt8(base_out, lora_out, m, n, s, y, z8, z_scale, bias=bias)
     where = "dora_compose_fwd_ckpt8"
-    _acts2d(base_out, where)
-    tokens, d_out = base_out.shape
-    _like(base_out, where, lora_out=lora_out, y=y)
-    _vec_f32(d_out, where, m=m, n=n)
-    _check_bias(bias, base_out, where)
-    z8, z_scale = _checkpoint(where, tokens, d_out, z8, z_scale, base_out.device)
-    _dense_cuda(base_out, lora_out, m, n, y, z8, z_scale, bias)
+    if base_out.dim() != 2:
+        _acts2d(base_out, where)
+    dt, shape, dtype = _dt(base_out), base_out.shape, base_out.dtype
+    tokens, d_out = shape
+    if lora_out.dtype is not dtype or lora_out.shape != shape or y is not None:
+        _like(base_out, where, lora_out=lora_out, y=y)
+    if m.dtype is not torch.float32 or n.dtype is not torch.float32 or m.shape != (d_out,) or n.shape != (d_out,):
+        _vec_f32(d_out, where, m=m, n=n)
+    if bias is not None:
+        _check_bias(bias, base_out, where)
+    blocks = -(-d_out // CKPT_BLOCK)
+    if z8 is not None:
+        _typed(where, "z8", z8, shape, torch.int8)
+    if z_scale is not None:
+        _typed(where, "z_scale", z_scale, (tokens, blocks), torch.float32)
+    dev = _dense_cuda(base_out, lora_out, m, n, y, z8, z_scale, bias)
     if y is None:
         y = torch.empty_like(base_out)
+    if z8 is None:
+        z8 = torch.empty_like(base_out, dtype=torch.int8)
+    if z_scale is None:
+        z_scale = base_out.new_empty((tokens, blocks), dtype=torch.float32)
     st = lib().dora_compose_fwd_ckpt8(
-        _ptr(base_out), _ptr(lora_out), _ptr(bias), _ptr(m), _ptr(n), float(s), tokens, d_out, _dt(base_out), _ptr(y),
-        _ptr(z8), _ptr(z_scale), _stream(),
+        base_out.data_ptr(), lora_out.data_ptr(), _ptr(bias), m.data_ptr(), n.data_ptr(), s, tokens, d_out, dt,
+        y.data_ptr(), z8.data_ptr(), z_scale.data_ptr(), _raw_stream(dev),
     )
     _check(st, where)
     return y, z8, z_scale
@@ -748,25 +792,32 @@ def dora_compose_bwd_ckpt8(dy, z8, z_scale, m, n, s: float, d_base=None, d_lora=
         with torch.cuda.stream(stream):
             return dora_compose_bwd_ckpt8(dy, z8, z_scale, m, n, s, d_base, d_lora, d_m, workspace)
     where = "dora_compose_bwd_ckpt8"
-    _acts2d(dy, where)
-    tokens, d_out = dy.shape
-    _like(dy, where, d_base=d_base, d_lora=d_lora)
-    _vec_f32(d_out, where, m=m, n=n, d_m=d_m)
-    _typed(where, "z8", z8, (tokens, d_out), torch.int8)
-    _typed(where, "z_scale", z_scale, (tokens, -(-d_out // CKPT_BLOCK)), torch.float32)
-    _dense_cuda(dy, z8, z_scale, m, n, d_base, d_lora, d_m, workspace)
+    if dy.dim() != 2:
+        _acts2d(dy, where)
+    dt, shape = _dt(dy), dy.shape
+    tokens, d_out = shape
+    if d_base is not None or d_lora is not None:
+        _like(dy, where, d_base=d_base, d_lora=d_lora)
+    if (m.dtype is not torch.float32 or n.dtype is not torch.float32 or m.shape != (d_out,) or n.shape != (d_out,)
+            or d_m is not None):
+        _vec_f32(d_out, where, m=m, n=n, d_m=d_m)
+    scales = (tokens, -(-d_out // CKPT_BLOCK))
+    if z8.dtype is not torch.int8 or z_scale.dtype is not torch.float32 or z8.shape != shape or z_scale.shape != scales:
+        _typed(where, "z8", z8, shape, torch.int8)
+        _typed(where, "z_scale", z_scale, scales, torch.float32)
+    dev = _dense_cuda(dy, z8, z_scale, m, n, d_base, d_lora, d_m, workspace)
     if d_base is None:
         d_base = torch.empty_like(dy)
     if d_lora is None:
         d_lora = torch.empty_like(dy)
     if d_m is None:
-        d_m = torch.empty(d_out, dtype=torch.float32, device=dy.device)
+        d_m = torch.empty_like(m)
     if workspace is None:
-        workspace = torch.empty(dora_compose_bwd_ckpt8_workspace_size(tokens, d_out), dtype=torch.uint8,
-                                device=dy.device)
+        workspace = dy.new_empty(lib().dora_compose_bwd_ckpt8_workspace_size(tokens, d_out), dtype=torch.uint8)
     st = lib().dora_compose_bwd_ckpt8(
-        _ptr(dy), _ptr(z8), _ptr(z_scale), _ptr(m), _ptr(n), float(s), tokens, d_out, _dt(dy), _ptr(d_base),
-        _ptr(d_lora), _ptr(d_m), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(),
+        dy.data_ptr(), z8.data_ptr(), z_scale.data_ptr(), m.data_ptr(), n.data_ptr(), s, tokens, d_out, dt,
+        d_base.data_ptr(), d_lora.data_ptr(), d_m.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(dev),
     )
     _check(st, where)
     return d_base, d_lora, d_m
