@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(256, 2) compose_fwd_ckpt8_kernel(
   const int gl = threadIdx.x % L::kLanes;
   const long long block = blockIdx.x * static_cast<long long>(blockDim.x / L::kLanes) + threadIdx.x / L::kLanes;
   const uint32_t group = L::kLanes == 32 ? 0xFFFFFFFFu : 0xFFFFu << (threadIdx.x & 16);
+  after_previous();
   if (block >= blocks) return;  // a whole group of lanes
   const long long col0 = block * kCkptBlock;
   const long long left = d_out - col0;
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(kCkptBwdThreads) compose_bwd_ckpt8_kernel(
   const long long block = blockIdx.x;
   const long long col0 = block * kCkptBlock;
   const long long left = d_out - col0;
+  after_previous();
   float g[E], acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {

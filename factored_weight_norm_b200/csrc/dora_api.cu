@@ -291,6 +291,23 @@ size_t f32_norm_ws(int64_t r) { return align_up(static_cast<size_t>(r) * r * 4, 
 
 int launch_error() { return cudaGetLastError() == cudaSuccess ? DORA_OK : DORA_ERR_CUDA; }
 
+// Launches a kernel that starts under the launch before it and waits itself for
+// that launch's end (programmatic dependent launch).
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? DORA_OK : DORA_ERR_CUDA;
+}
+
 // Resident CTAs per SM of a kernel at the given block size (at least 1).
 template <typename K>
 int ctas_per_sm(K kernel, int threads) {
@@ -1091,7 +1108,7 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
     ca.wait_limit = kWaitLimitCycles;
     ca.status = dev->status;
     cudaLaunchConfig_t cfg = pair_config(attrs, kI8Threads, linear_i8_smem(dev->smem_optin),
-                                         static_cast<long long>(ca.tiles_m) * ca.tiles_n, r > 0, dev, st);
+                                         static_cast<long long>(ca.tiles_m) * ca.tiles_n, true, dev, st);
     note_launch();
     if (cudaLaunchKernelEx(&cfg, linear_ckpt8_pair_kernel, tmX, tmW, r > 0 ? tmP : tmX, r > 0 ? tmLo : tmX,
                            r > 0 ? tmB : tmW, ca) != cudaSuccess)
@@ -1167,20 +1184,16 @@ namespace {
 template <typename T, int VEC, bool HAS_W>
 int launch_rows_i8(const RowsI8Args& a, const DeviceInfo* dev, cudaStream_t st) {
   const long long most = VEC == 1 || a.rows < 2LL * dev->num_sms ? 1024 : 64;
-  const unsigned grid = static_cast<unsigned>(a.rows);
+  const dim3 grid(static_cast<unsigned>(a.rows));
   const auto threads = [&](long long nv) { return static_cast<unsigned>(align_up(cdiv(cdiv(a.d, VEC), nv), 32)); };
-  note_launch();
-  if (cdiv(a.d, 8) <= most)
-    rows_i8_kernel<T, VEC, 8 / VEC, 1024, HAS_W><<<grid, threads(8 / VEC), 0, st>>>(a);
-  else if (cdiv(a.d, 16) <= most)
-    rows_i8_kernel<T, VEC, 16 / VEC, 1024, HAS_W><<<grid, threads(16 / VEC), 0, st>>>(a);
-  else if (cdiv(a.d, 32) <= 256)
-    rows_i8_kernel<T, VEC, 32 / VEC, 256, HAS_W><<<grid, threads(32 / VEC), 0, st>>>(a);
-  else if (cdiv(a.d, 32) <= 1024)
-    rows_i8_kernel<T, VEC, 32 / VEC, 1024, HAS_W><<<grid, threads(32 / VEC), 0, st>>>(a);
-  else
-    rows_i8_long_kernel<T, VEC><<<grid, 1024, 0, st>>>(a);
-  return launch_error();
+  if (cdiv(a.d, 8) <= most) return launch_after(rows_i8_kernel<T, VEC, 8 / VEC, 1024, HAS_W>, grid, threads(8 / VEC), st, a);
+  if (cdiv(a.d, 16) <= most)
+    return launch_after(rows_i8_kernel<T, VEC, 16 / VEC, 1024, HAS_W>, grid, threads(16 / VEC), st, a);
+  if (cdiv(a.d, 32) <= 256)
+    return launch_after(rows_i8_kernel<T, VEC, 32 / VEC, 256, HAS_W>, grid, threads(32 / VEC), st, a);
+  if (cdiv(a.d, 32) <= 1024)
+    return launch_after(rows_i8_kernel<T, VEC, 32 / VEC, 1024, HAS_W>, grid, threads(32 / VEC), st, a);
+  return launch_after(rows_i8_long_kernel<T, VEC>, grid, 1024, st, a);
 }
 
 template <typename T, int VEC>
@@ -1222,7 +1235,7 @@ int rows_i8(const void* x, const void* residual, const void* weight, bool norm, 
 }
 
 template <typename L>
-void launch_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const void* bias, const float* m,
+int launch_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const void* bias, const float* m,
                               const float* n, float s, int64_t tokens, int64_t d_out, void* y, int8_t* z8,
                               float* z_scale, const DeviceInfo* dev, cudaStream_t st) {
   using T = typename L::T;
@@ -1233,15 +1246,14 @@ void launch_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const 
   // keeps the next group's in flight (at 8192 x 8192 bf16 87.6 us; 90.7 with 8
   // CTAs an SM in turn, 103.6 with 16)
   const long long gy = std::max<long long>(1, std::min<long long>({2LL * dev->num_sms / gx, cdiv(tokens, kCkptRows), 65535}));
-  note_launch();
-  (bias ? compose_fwd_ckpt8_kernel<L, true> : compose_fwd_ckpt8_kernel<L, false>)<<<
-      dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), threads, 0, st>>>(
-      static_cast<const T*>(base_out), static_cast<const T*>(lora_out), static_cast<const T*>(bias), m, n, s, tokens,
-      d_out, blocks, static_cast<T*>(y), z8, z_scale);
+  return launch_after(bias ? compose_fwd_ckpt8_kernel<L, true> : compose_fwd_ckpt8_kernel<L, false>,
+                      dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), threads, st,
+                      static_cast<const T*>(base_out), static_cast<const T*>(lora_out), static_cast<const T*>(bias), m, n,
+                      s, tokens, d_out, blocks, static_cast<T*>(y), z8, z_scale);
 }
 
 template <typename L>
-void launch_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_scale, const float* m, const float* n,
+int launch_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_scale, const float* m, const float* n,
                               float s, int64_t tokens, int64_t d_out, void* d_base, void* d_lora, float* d_m,
                               uint8_t* ws, const DeviceInfo* dev, cudaStream_t st) {
   using T = typename L::T;
@@ -1254,11 +1266,9 @@ void launch_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_s
       std::max<long long>(1, std::min<long long>({slots / blocks, static_cast<long long>(kCkptMaxChunks), most}));
   unsigned long long* marks = reinterpret_cast<unsigned long long*>(ws);  // tagged: no clearing needed
   float* part = reinterpret_cast<float*>(ws + blocks * kCkptMaxChunks * 8);
-  note_launch();
-  compose_bwd_ckpt8_kernel<L><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(chunks)),
-                                kCkptBwdThreads, 0, st>>>(
-      static_cast<const T*>(dy), z8, z_scale, m, n, s, tokens, d_out, blocks, static_cast<T*>(d_base),
-      static_cast<T*>(d_lora), part, marks, d_m, next_bwd_epoch() + 1);
+  return launch_after(compose_bwd_ckpt8_kernel<L>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(chunks)),
+                      kCkptBwdThreads, st, static_cast<const T*>(dy), z8, z_scale, m, n, s, tokens, d_out, blocks,
+                      static_cast<T*>(d_base), static_cast<T*>(d_lora), part, marks, d_m, next_bwd_epoch() + 1);
 }
 
 }  // namespace
@@ -1298,24 +1308,17 @@ int dora_dequantize_i8(const int8_t* q, const float* scale, int64_t rows, int64_
     // 4099 fp32: 13.5 us, 17.6 with 32; 8192 x 8192 bf16: 31.7, 34.1 with 8)
     const long long ctas = (vec > 1 ? 32LL : 8LL) * dev->num_sms;
     const long long gy = std::max<long long>(1, std::min<long long>({cdiv(rows, u), 65535, ctas / gx}));
-    note_launch();
-    kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), threads, 0, st>>>(q, scale, rows, cols, width,
-                                                                                           blocks, o);
+    return launch_after(kernel, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), threads, st, q, scale, rows,
+                        cols, width, blocks, o);
   };
   if (dt == DORA_BF16) {
     auto* o = static_cast<__nv_bfloat16*>(out);
-    if (cols % 8 == 0 && aligned(q, 8) && aligned(out, 16))
-      launch(dequant_i8_kernel<__nv_bfloat16, 8, 4>, 8, 4, o);
-    else
-      launch(dequant_i8_kernel<__nv_bfloat16, 1, 8>, 1, 8, o);
-  } else {
-    auto* o = static_cast<float*>(out);
-    if (cols % 4 == 0 && aligned(q, 4) && aligned(out, 16))
-      launch(dequant_i8_kernel<float, 4, 4>, 4, 4, o);
-    else
-      launch(dequant_i8_kernel<float, 1, 8>, 1, 8, o);
+    if (cols % 8 == 0 && aligned(q, 8) && aligned(out, 16)) return launch(dequant_i8_kernel<__nv_bfloat16, 8, 4>, 8, 4, o);
+    return launch(dequant_i8_kernel<__nv_bfloat16, 1, 8>, 1, 8, o);
   }
-  return launch_error();
+  auto* o = static_cast<float*>(out);
+  if (cols % 4 == 0 && aligned(q, 4) && aligned(out, 16)) return launch(dequant_i8_kernel<float, 4, 4>, 4, 4, o);
+  return launch(dequant_i8_kernel<float, 1, 8>, 1, 8, o);
 }
 
 size_t dora_linear_i8_fwd_workspace_size(int64_t tokens, int64_t r) {
@@ -1365,7 +1368,7 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
     sa.n = n;
     sa.bias = static_cast<const __nv_bfloat16*>(bias);
     sa.out = static_cast<__nv_bfloat16*>(y);
-    return launch_slice(true, tmWq, tmXq, r > 0 ? tmB : tmWq, r > 0 ? tmP : tmXq, sa, r > 0, 0, dev, st);
+    return launch_slice(true, tmWq, tmXq, r > 0 ? tmB : tmWq, r > 0 ? tmP : tmXq, sa, true, 0, dev, st);
   }
   const long long tiles_m = cdiv(tokens, kPairBM);
   const int bn = pick_bn_waves(tiles_m, d_out, dev);
@@ -1392,7 +1395,7 @@ int dora_linear_i8_fwd(const int8_t* x_q, const float* x_scale, const int8_t* W_
   la.status = dev->status;
   cudaLaunchAttribute attrs[2];
   cudaLaunchConfig_t cfg = pair_config(attrs, kI8Threads, linear_i8_smem(dev->smem_optin),
-                                       static_cast<long long>(la.tiles_m) * la.tiles_n, r > 0, dev, st);
+                                       static_cast<long long>(la.tiles_m) * la.tiles_n, true, dev, st);
   note_launch();
   if (cudaLaunchKernelEx(&cfg, linear_i8_pair_kernel, tmXq, tmWq, r > 0 ? tmP : tmXq, r > 0 ? tmB : tmWq, la) !=
       cudaSuccess)
@@ -1417,12 +1420,10 @@ int dora_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const voi
   if (device_info(&dev)) return DORA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dt == DORA_BF16)
-    launch_compose_fwd_ckpt8<LanesBf16>(base_out, lora_out, bias, m, n, s, tokens, d_out, y, z8, z_scale, dev, st);
-  else if (d_out % 4 == 0 && all_aligned(16) && aligned(z8, 4))
-    launch_compose_fwd_ckpt8<LanesF32>(base_out, lora_out, bias, m, n, s, tokens, d_out, y, z8, z_scale, dev, st);
-  else
-    launch_compose_fwd_ckpt8<LanesF32Any>(base_out, lora_out, bias, m, n, s, tokens, d_out, y, z8, z_scale, dev, st);
-  return launch_error();
+    return launch_compose_fwd_ckpt8<LanesBf16>(base_out, lora_out, bias, m, n, s, tokens, d_out, y, z8, z_scale, dev, st);
+  if (d_out % 4 == 0 && all_aligned(16) && aligned(z8, 4))
+    return launch_compose_fwd_ckpt8<LanesF32>(base_out, lora_out, bias, m, n, s, tokens, d_out, y, z8, z_scale, dev, st);
+  return launch_compose_fwd_ckpt8<LanesF32Any>(base_out, lora_out, bias, m, n, s, tokens, d_out, y, z8, z_scale, dev, st);
 }
 
 size_t dora_compose_bwd_ckpt8_workspace_size(int64_t tokens, int64_t d_out) {
@@ -1455,12 +1456,10 @@ int dora_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_scal
     return cudaMemsetAsync(d_m, 0, static_cast<size_t>(d_out) * 4, st) == cudaSuccess ? DORA_OK : DORA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (dt == DORA_BF16)
-    launch_compose_bwd_ckpt8<LanesBf16>(dy, z8, z_scale, m, n, s, tokens, d_out, d_base, d_lora, d_m, ws, dev, st);
-  else if (d_out % 4 == 0 && all_aligned(16) && aligned(z8, 4))
-    launch_compose_bwd_ckpt8<LanesF32>(dy, z8, z_scale, m, n, s, tokens, d_out, d_base, d_lora, d_m, ws, dev, st);
-  else
-    launch_compose_bwd_ckpt8<LanesF32Any>(dy, z8, z_scale, m, n, s, tokens, d_out, d_base, d_lora, d_m, ws, dev, st);
-  return launch_error();
+    return launch_compose_bwd_ckpt8<LanesBf16>(dy, z8, z_scale, m, n, s, tokens, d_out, d_base, d_lora, d_m, ws, dev, st);
+  if (d_out % 4 == 0 && all_aligned(16) && aligned(z8, 4))
+    return launch_compose_bwd_ckpt8<LanesF32>(dy, z8, z_scale, m, n, s, tokens, d_out, d_base, d_lora, d_m, ws, dev, st);
+  return launch_compose_bwd_ckpt8<LanesF32Any>(dy, z8, z_scale, m, n, s, tokens, d_out, d_base, d_lora, d_m, ws, dev, st);
 }
 
 // ---------------------------------------------------- attached-norm backward

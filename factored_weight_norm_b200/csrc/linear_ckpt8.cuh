@@ -107,6 +107,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+  // without an adapter the launch before may be anything; with one it is P's,
+  // which itself came after all others, and only P has to be waited for
+  if (a.kb_r == 0) grid_dep_wait();
+  grid_dep_launch();
 
   if (warp < 4) {
     regs_give<kI8RegsFew>();

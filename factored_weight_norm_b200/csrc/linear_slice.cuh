@@ -253,7 +253,10 @@ __global__ void __launch_bounds__(kSlThreads)
     tma_load_2d(dst, ext ? &tmB : &tmW, &full[stage], xk, row0);
     tma_load_2d(dst + kLinABytes, ext ? &tmP : &tmX, &full[stage], xk, tok0);
   };
-  // the first fills wait for nothing, so they go out before the rest is set up
+  // without an adapter the launch before may be anything; with one it is P's,
+  // which itself came after all others, and only P has to be waited for
+  const bool wait_all = I8 && a.kb_total == a.kb_main;
+  // the first fills wait for nothing else, so they go out before the rest is set up
   const int early = min(stages, min(kb1, a.kb_main) - kb0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -262,6 +265,7 @@ __global__ void __launch_bounds__(kSlThreads)
     }
     mbar_init(acc_full, 1);
     fence_mbar_init();
+    if (wait_all) grid_dep_wait();
     for (int s = 0; s < early; ++s) fill(s, kb0 + s);
   }
   if (warp == 1) {
@@ -272,6 +276,7 @@ __global__ void __launch_bounds__(kSlThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (wait_all) grid_dep_wait();
   grid_dep_launch();
 
   if (warp == 0) {

@@ -401,3 +401,89 @@ def test_linear_i8_of_millions_of_tokens():
     rows = np.array([0, 1, 127, 255, 4_000_000, 8_388_607, 8_388_608, T - 1])
     small = {n: (k[n] if n not in ("x_q", "x_scale", "x") else k[n][torch.as_tensor(rows, device=DEV)]) for n in k}
     _check_linear(small, y[torch.as_tensor(rows, device=DEV)])
+
+
+@pytest.mark.parametrize("r", [0, 64])
+def test_captured_behind_anything_and_before_anything(r):
+    # the calls start under the launch before them: that launch may be nothing
+    # (the graph's first node), a copy, a memset, another library's kernel, the
+    # join of two streams, or a long kernel whose output the call reads
+    T, d = 96, 1024
+    k = _module(T, d, 520, r, seed=71)
+    w = torch.ones(d, dtype=BF, device=DEV)
+    src, x, res = _rows(T, d, BF, 72), _rows(T, d, BF, 73), _rows(T, d, BF, 74)
+    q, sc, y = torch.empty(T, d, dtype=torch.int8, device=DEV), torch.empty(T, device=DEV), torch.empty_like(x)
+    out, val = torch.empty(T, 520, dtype=BF, device=DEV), torch.empty_like(x)
+    ws = torch.empty(max(256, D.dora_linear_i8_fwd_workspace_size(T, r)), dtype=torch.uint8, device=DEV)
+    late = torch.randn(2048, 2048, device=DEV)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    lin = {**k, "x_q": q, "x_scale": sc, **({"x": y} if r else {})}
+
+    def chain(where):
+        main = torch.cuda.current_stream()
+        if where == "copy":
+            x.copy_(src)
+        elif where == "memset":
+            res.zero_()
+        elif where == "kernel":
+            torch.mul(src, 0.5, out=x)
+        elif where == "join":
+            for st, (dst, f) in zip(side, ((x, 2.0), (res, 0.25))):
+                st.wait_stream(main)
+                with torch.cuda.stream(st):
+                    torch.mul(src, f, out=dst)
+            for st in side:
+                main.wait_stream(st)
+        elif where == "late":
+            m = late
+            for _ in range(6):
+                m = (m @ late) * 1e-2
+            x.copy_(src + m[:T, :d].to(BF) * 0)
+        D.dora_rms_norm_i8(x, w, residual=res, h=res, q=q, scale=sc, y=y)
+        D.dora_linear_i8_fwd(**lin, y=out, workspace=ws)
+        D.dora_dequantize_i8(q, sc, out=val)
+        if where != "first":
+            torch.add(val, y, out=x)  # overwrites what the chain has read
+            D.dora_quantize_rows_i8(x, q=q, scale=sc)
+            D.dora_linear_i8_fwd(**lin, y=out, workspace=ws)
+
+    for where in ("first", "copy", "memset", "kernel", "join", "late"):
+        chain(where)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain(where)
+        for _ in range(3):
+            res.copy_(_rows(T, d, BF, 75))
+            x.copy_(_rows(T, d, BF, 76))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in (res, x, q, sc, y, out, val)]
+            res.copy_(_rows(T, d, BF, 75))
+            x.copy_(_rows(T, d, BF, 76))
+            chain(where)
+            torch.cuda.synchronize()
+            for a, b in zip(got, (res, x, q, sc, y, out, val)):
+                assert torch.equal(a, b), where
+        _check_linear(lin, out)
+    assert D.dora_device_status() == D.DORA_OK
+
+
+def test_back_to_back_calls_see_each_other_s_results():
+    # dependent launches in one stream, outputs overwritten while the next call waits
+    T, d = 2048, 2048
+    x = _rows(T, d, BF, 81)
+    acc = torch.zeros_like(x)
+    ref = torch.zeros_like(x)
+    for i in range(6):
+        q, sc, h = D.dora_quantize_rows_i8(x, residual=acc, h=acc)
+        v = D.dora_dequantize_i8(q, sc)
+        acc.sub_(v)  # what the codes lost
+    torch.cuda.synchronize()
+    for i in range(6):
+        ref = (x.float() + ref.float()).to(BF)
+        codes, sc64 = oracle.encode(P.f64(ref))
+        val = (torch.from_numpy(codes).float() * torch.from_numpy(sc64.astype(np.float32))).to(BF).to(DEV)
+        ref = ref - val
+    assert torch.equal(acc, ref)
