@@ -458,37 +458,13 @@ def dora_fused_linear_fwd_workspace_size(tokens: int, r: int) -> int:
 
 def dora_fused_linear_fwd(x, W, A, B, m, n, s: float, bias=None, y=None, workspace=None, stream=None):
     """y = b + (m / n) * (x W^T + s * (x A^T) B^T), the compose fused into the GEMMs (bf16)."""
-    return _fused_linear("dora_fused_linear_fwd", x, W, A, B, m, n, s, bias, y, None, None, workspace, stream)
-
-
-def dora_fused_linear_fwd_ckpt8_workspace_size(tokens: int, r: int) -> int:
-    return int(lib().dora_fused_linear_fwd_ckpt8_workspace_size(tokens, r))
-
-
-def dora_fused_linear_fwd_ckpt8(x, W, A, B, m, n, s: float, bias=None, y=None, z8=None, z_scale=None, workspace=None,
-                                stream=None):
-    """dora_fused_linear_fwd that keeps z = x W^T + s * (x A^T) B^T for the backward: (y, z8, z_scale).
-
-    z8 are int8 codes [tokens, d_out], z_scale their fp32 scales for every 128
-    columns of a token; ``dora_compose_bwd_ckpt8`` reads them."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return dora_fused_linear_fwd_ckpt8(x, W, A, B, m, n, s, bias, y, z8, z_scale, workspace)
-    where = "dora_fused_linear_fwd_ckpt8"
-    if x.dim() != 2 or W.dim() != 2:
-        raise ValueError(f"{where}: x, W, A and B must be 2-D")
-    z8, z_scale = _checkpoint(where, x.shape[0], W.shape[0], z8, z_scale, x.device)
-    y = _fused_linear(where, x, W, A, B, m, n, s, bias, y, z8, z_scale, workspace, stream)
-    return y, z8, z_scale
-
-
-def _fused_linear(where, x, W, A, B, m, n, s, bias, y, z8, z_scale, workspace, stream):
+    where = "dora_fused_linear_fwd"
     if x.dim() != 2 or W.dim() != 2 or A.dim() != 2 or B.dim() != 2:
         raise ValueError(f"{where}: x, W, A and B must be 2-D")
     T, d_in = x.shape
     d_out, r = W.shape[0], A.shape[0]
     if W.shape != (d_out, d_in) or A.shape != (r, d_in) or B.shape != (d_out, r):
-        raise ValueError(f"shape mismatch in {where}")
+        raise ValueError("shape mismatch in dora_fused_linear_fwd")
     _vec_f32(d_out, where, m=m, n=n)
     for t in (x, W, A, B):
         if t.dtype != torch.bfloat16:
@@ -497,20 +473,17 @@ def _fused_linear(where, x, W, A, B, m, n, s, bias, y, z8, z_scale, workspace, s
         raise ValueError("bias must be bf16 of shape (d_out,)")
     if y is not None and (tuple(y.shape) != (T, d_out) or y.dtype != torch.bfloat16):
         raise ValueError(f"{where}: y must be bf16 of shape ({T}, {d_out})")
-    _dense_cuda(x, W, A, B, m, n, bias, y, z8, z_scale, workspace)
+    _dense_cuda(x, W, A, B, m, n, bias, y, workspace)
     if y is None:
         y = torch.empty(T, d_out, dtype=torch.bfloat16, device=x.device)
+    need = dora_fused_linear_fwd_workspace_size(T, r)
     if workspace is None:
-        size = dora_fused_linear_fwd_workspace_size if z8 is None else dora_fused_linear_fwd_ckpt8_workspace_size
-        workspace = torch.empty(size(T, r), dtype=torch.uint8, device=x.device)
-    head = (_ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(bias), _ptr(m), _ptr(n), float(s), T, d_in, d_out, r, DORA_BF16,
-            _ptr(y))
-    tail = (_ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
-    if z8 is None:
-        st = lib().dora_fused_linear_fwd(*head, *tail)
-    else:
-        st = lib().dora_fused_linear_fwd_ckpt8(*head, _ptr(z8), _ptr(z_scale), *tail)
-    _check(st, where)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    st = lib().dora_fused_linear_fwd(
+        _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(bias), _ptr(m), _ptr(n), float(s), T, d_in, d_out, r, DORA_BF16,
+        _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream),
+    )
+    _check(st, "dora_fused_linear_fwd")
     return y
 
 
@@ -570,18 +543,6 @@ def _typed(where: str, name: str, t, shape, dtype):
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
-
-
-def _checkpoint(where, tokens, d_out, z8, z_scale, device):
-    """(z8, z_scale) of a [tokens, d_out] checkpoint, checked or made."""
-    blocks = -(-d_out // CKPT_BLOCK)
-    _typed(where, "z8", z8, (tokens, d_out), torch.int8)
-    _typed(where, "z_scale", z_scale, (tokens, blocks), torch.float32)
-    if z8 is None:
-        z8 = torch.empty((tokens, d_out), dtype=torch.int8, device=device)
-    if z_scale is None:
-        z_scale = torch.empty((tokens, blocks), dtype=torch.float32, device=device)
-    return z8, z_scale
 
 
 def _rows_i8(where, x, residual, weight, h, y, q, scale):
@@ -646,7 +607,7 @@ def dora_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, want_y: bool =
     rows, cols, dt, h, q, scale, st = _rows_i8(where, x, residual, weight, h, y, q, scale)
     if y is None and want_y:
         y = torch.empty_like(x)
-    _check(lib().dora_rms_norm_i8(x.data_ptr(), _ptr(residual), weight.data_ptr(), eps, rows, cols, dt, _ptr(h),
+    _check(lib().dora_rms_norm_i8(x.data_ptr(), _ptr(residual), weight.data_ptr(), float(eps), rows, cols, dt, _ptr(h),
                                   _ptr(y), q.data_ptr(), scale.data_ptr(), st), where)
     return q, scale, h, y
 
@@ -735,7 +696,7 @@ def dora_linear_i8_fwd(x_q, x_scale, W_q, w_scale, x=None, A=None, B=None, m=Non
         workspace = x_q.new_empty(lib().dora_linear_i8_fwd_workspace_size(T, r), dtype=torch.uint8)
     st = lib().dora_linear_i8_fwd(
         x_q.data_ptr(), x_scale.data_ptr(), W_q.data_ptr(), w_scale.data_ptr(), _ptr(x), _ptr(A), _ptr(B), _ptr(bias),
-        _ptr(m), _ptr(n), s, T, d_in, d_out, r, DORA_BF16, y.data_ptr(), _ptr(workspace),
+        _ptr(m), _ptr(n), float(s), T, d_in, d_out, r, DORA_BF16, y.data_ptr(), _ptr(workspace),
         0 if workspace is None else workspace.nbytes, _raw_stream(dev),
     )
     _check(st, where)
@@ -774,7 +735,7 @@ def dora_compose_fwd_ckpt8(base_out, lora_out, m, n, s: float, y=None, z8=None, 
     if z_scale is None:
         z_scale = base_out.new_empty((tokens, blocks), dtype=torch.float32)
     st = lib().dora_compose_fwd_ckpt8(
-        base_out.data_ptr(), lora_out.data_ptr(), _ptr(bias), m.data_ptr(), n.data_ptr(), s, tokens, d_out, dt,
+        base_out.data_ptr(), lora_out.data_ptr(), _ptr(bias), m.data_ptr(), n.data_ptr(), float(s), tokens, d_out, dt,
         y.data_ptr(), z8.data_ptr(), z_scale.data_ptr(), _raw_stream(dev),
     )
     _check(st, where)
@@ -815,9 +776,63 @@ def dora_compose_bwd_ckpt8(dy, z8, z_scale, m, n, s: float, d_base=None, d_lora=
     if workspace is None:
         workspace = dy.new_empty(lib().dora_compose_bwd_ckpt8_workspace_size(tokens, d_out), dtype=torch.uint8)
     st = lib().dora_compose_bwd_ckpt8(
-        dy.data_ptr(), z8.data_ptr(), z_scale.data_ptr(), m.data_ptr(), n.data_ptr(), s, tokens, d_out, dt,
+        dy.data_ptr(), z8.data_ptr(), z_scale.data_ptr(), m.data_ptr(), n.data_ptr(), float(s), tokens, d_out, dt,
         d_base.data_ptr(), d_lora.data_ptr(), d_m.data_ptr(), workspace.data_ptr(), workspace.nbytes,
         _raw_stream(dev),
     )
     _check(st, where)
     return d_base, d_lora, d_m
+
+
+def dora_fused_linear_fwd_ckpt8_workspace_size(tokens: int, r: int) -> int:
+    return int(lib().dora_fused_linear_fwd_ckpt8_workspace_size(tokens, r))
+
+
+def dora_fused_linear_fwd_ckpt8(x, W, A, B, m, n, s: float, bias=None, y=None, z8=None, z_scale=None, workspace=None,
+                                stream=None):
+    """dora_fused_linear_fwd that keeps z = x W^T + s * (x A^T) B^T for the backward: (y, z8, z_scale).
+
+    z8 are int8 codes [tokens, d_out], z_scale their fp32 scales for every 128
+    columns of a token; ``dora_compose_bwd_ckpt8`` reads them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dora_fused_linear_fwd_ckpt8(x, W, A, B, m, n, s, bias, y, z8, z_scale, workspace)
+    where = "dora_fused_linear_fwd_ckpt8"
+    if x.dim() != 2 or W.dim() != 2 or A.dim() != 2 or B.dim() != 2:
+        raise ValueError(f"{where}: x, W, A and B must be 2-D")
+    bf16, f32 = torch.bfloat16, torch.float32
+    T, d_in = x.shape
+    d_out, r = W.shape[0], A.shape[0]
+    if (x.dtype is not bf16 or W.dtype is not bf16 or A.dtype is not bf16 or B.dtype is not bf16
+            or W.shape != (d_out, d_in) or A.shape != (r, d_in) or B.shape != (d_out, r)):
+        _typed(where, "x", x, (T, d_in), bf16)
+        _typed(where, "W", W, (d_out, d_in), bf16)
+        _typed(where, "A", A, (r, d_in), bf16)
+        _typed(where, "B", B, (d_out, r), bf16)
+    if m.dtype is not f32 or n.dtype is not f32 or m.shape != (d_out,) or n.shape != (d_out,):
+        _vec_f32(d_out, where, m=m, n=n)
+    blocks = -(-d_out // CKPT_BLOCK)
+    if bias is not None:
+        _typed(where, "bias", bias, (d_out,), bf16)
+    if y is not None:
+        _typed(where, "y", y, (T, d_out), bf16)
+    if z8 is not None:
+        _typed(where, "z8", z8, (T, d_out), torch.int8)
+    if z_scale is not None:
+        _typed(where, "z_scale", z_scale, (T, blocks), f32)
+    dev = _dense_cuda(x, W, A, B, m, n, bias, y, z8, z_scale, workspace)
+    if y is None:
+        y = x.new_empty((T, d_out))
+    if z8 is None:
+        z8 = torch.empty_like(y, dtype=torch.int8)
+    if z_scale is None:
+        z_scale = m.new_empty((T, blocks))
+    if workspace is None and r > 0:
+        workspace = x.new_empty(lib().dora_fused_linear_fwd_ckpt8_workspace_size(T, r), dtype=torch.uint8)
+    st = lib().dora_fused_linear_fwd_ckpt8(
+        x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), _ptr(bias), m.data_ptr(), n.data_ptr(), float(s), T,
+        d_in, d_out, r, DORA_BF16, y.data_ptr(), z8.data_ptr(), z_scale.data_ptr(), _ptr(workspace),
+        0 if workspace is None else workspace.nbytes, _raw_stream(dev),
+    )
+    _check(st, where)
+    return y, z8, z_scale
