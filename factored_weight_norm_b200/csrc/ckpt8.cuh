@@ -27,6 +27,7 @@ namespace dora {
 struct LanesBf16 {
   using T = __nv_bfloat16;
   using Raw = uint4;
+  static constexpr int kIndex = 0;
   static constexpr int kE = 8, kLanes = 16;
   static __device__ __forceinline__ int col(int gl, int e) { return gl * 8 + e; }
   static __device__ __forceinline__ bool any(int gl, long long left) { return gl * 8 < left; }
@@ -57,6 +58,7 @@ struct LanesBf16 {
 struct LanesF32 {
   using T = float;
   using Raw = uint4;
+  static constexpr int kIndex = 1;
   static constexpr int kE = 4, kLanes = 32;
   static __device__ __forceinline__ int col(int gl, int e) { return gl * 4 + e; }
   static __device__ __forceinline__ bool any(int gl, long long left) { return gl * 4 < left; }
@@ -81,6 +83,7 @@ struct LanesF32Any {
   struct Raw {
     float v[4];
   };
+  static constexpr int kIndex = 2;
   static constexpr int kE = 4, kLanes = 32;
   static __device__ __forceinline__ int col(int gl, int e) { return gl + 32 * e; }
   static __device__ __forceinline__ bool any(int gl, long long left) { return gl < left; }

@@ -99,12 +99,16 @@ constexpr int64_t kMaxRank = 4096;
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
+template <typename K>
+int ctas_per_sm(K kernel, int threads);
+
 struct DeviceInfo {
   bool ready = false;
   int num_sms = 0;
   int smem_optin = 0;
   int* status = nullptr;
   int pair_clusters = 0;  // co-resident 2-CTA clusters of linear_pair_kernel
+  int ckpt_bwd_ctas[3] = {1, 1, 1};  // resident CTAs per SM of compose_bwd_ckpt8_kernel, by L::kIndex
 };
 
 std::mutex g_mu;
@@ -171,6 +175,9 @@ int device_info(DeviceInfo** out) {
         pair_attrs(linear_pair_kernel<true, true>, d.smem_optin) ||
         pair_attrs(linear_i8_pair_kernel, d.smem_optin) || pair_attrs(linear_ckpt8_pair_kernel, d.smem_optin))
       return DORA_ERR_CUDA;
+    d.ckpt_bwd_ctas[LanesBf16::kIndex] = ctas_per_sm(compose_bwd_ckpt8_kernel<LanesBf16>, kCkptBwdThreads);
+    d.ckpt_bwd_ctas[LanesF32::kIndex] = ctas_per_sm(compose_bwd_ckpt8_kernel<LanesF32>, kCkptBwdThreads);
+    d.ckpt_bwd_ctas[LanesF32Any::kIndex] = ctas_per_sm(compose_bwd_ckpt8_kernel<LanesF32Any>, kCkptBwdThreads);
     for (int i8 = 0; i8 < 2; ++i8)
       for (int bn : {16, 32, 64, 128})
         if (cudaFuncSetAttribute(slice_kernel(i8 != 0, bn), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1258,7 +1265,7 @@ int launch_compose_bwd_ckpt8(const void* dy, const int8_t* z8, const float* z_sc
                               uint8_t* ws, const DeviceInfo* dev, cudaStream_t st) {
   using T = typename L::T;
   const long long blocks = cdiv(d_out, kCkptBlock);
-  const long long slots = static_cast<long long>(dev->num_sms) * ctas_per_sm(compose_bwd_ckpt8_kernel<L>, kCkptBwdThreads);
+  const long long slots = static_cast<long long>(dev->num_sms) * dev->ckpt_bwd_ctas[L::kIndex];
   // at least one row for each row of lanes
   const long long most = cdiv(tokens, kCkptBwdThreads / L::kLanes);
   // one wave of resident CTAs (32768 x 8192 bf16: 309.7 us, 320.6 in two)
