@@ -15,7 +15,8 @@
 // The meeting is what costs beyond the stream: it is done once for the whole
 // tile, by all warps, with the loads from all splits in flight together (in
 // two rounds of 64 tokens by four warps, split after split, 128 tokens took 10
-// of 25 us).
+// of 25 us).  Measured at 8192 x 8192: one token 16.6 us (67 MB streamed in 10 to
+// 11, 6 TB/s or more; 2.5 to the first bytes, 2.5 to join), 128 tokens 21.5.
 #pragma once
 
 #include "linear_i8.cuh"

@@ -304,3 +304,24 @@ def test_a_given_stream_runs_the_training_pair():
         gb = D.dora_compose_bwd_ckpt8(dy, got[1], got[2], m, n, 0.5, stream=side)
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((*got, *gb), (*ref, *back)))
+
+
+def test_fused_offsets_past_32_bits():
+    T, d_in, d_out, r = 70001, 16, 32768, 8
+    g = _gen(14)
+    x = torch.randn(T, d_in, generator=g).to(BF).to(DEV)
+    W = (0.1 * torch.randn(d_out, d_in, generator=g)).to(BF).to(DEV)
+    A = (0.1 * torch.randn(r, d_in, generator=g)).to(BF).to(DEV)
+    B = (0.1 * torch.randn(d_out, r, generator=g)).to(BF).to(DEV)
+    one = torch.ones(d_out, device=DEV)
+    y, z8, zs = D.dora_fused_linear_fwd_ckpt8(x, W, A, B, one, one, 0.5)
+    rows = torch.tensor([0, 65535, 65536, 70000], device=DEV)
+    ys, z8s, zss = D.dora_fused_linear_fwd_ckpt8(x[rows], W, A, B, one, one, 0.5)
+    torch.cuda.synchronize()
+    assert D.dora_device_status() == D.DORA_OK
+    # the small call sums P over another split of K, so its rounding may differ in the last bits
+    z = P.f64(x[rows]) @ P.f64(W).T + 0.5 * (P.f64(x[rows]) @ P.f64(A).T) @ P.f64(B).T
+    for yy, cc, ss in ((y[rows], z8[rows], zs[rows]), (ys, z8s, zss)):
+        half = 0.5 * ss.cpu().double().numpy()[:, np.arange(d_out) // 128]
+        assert np.all(np.abs(oracle.decode(cc.cpu().numpy(), ss.cpu().numpy(), 128) - z) <= half + 64 * E * (1 + np.abs(z)))
+        assert np.all(np.abs(P.f64(yy) - z) <= U * np.abs(z) + 64 * E * (1 + np.abs(z)))

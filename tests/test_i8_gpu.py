@@ -487,3 +487,31 @@ def test_back_to_back_calls_see_each_other_s_results():
         val = (torch.from_numpy(codes).float() * torch.from_numpy(sc64.astype(np.float32))).to(BF).to(DEV)
         ref = ref - val
     assert torch.equal(acc, ref)
+
+
+def test_offsets_past_32_bits():
+    # rows and products with more than 2^31 elements: the last ones against fp64
+    T, d = 262160, 8192
+    x = torch.zeros(T, d, dtype=BF, device=DEV)
+    x[-3:] = _rows(3, d, BF, 91)
+    w = torch.ones(d, dtype=BF, device=DEV)
+    q, sc, _, y = D.dora_rms_norm_i8(x, w, 1e-5, want_y=True)
+    torch.cuda.synchronize()
+    # three rows by themselves would take more threads a row and add the squares in
+    # another order, so the norm's factor is held to fp64, not to a small call's bits:
+    # d non-negative terms in fp32 add at most d E to the sum, half of that to its
+    # root, and the mean, eps, root, reciprocal and product 5 E (as test_rms_norm)
+    codes, ref_sc, v = _norm_reference(x[-3:], w, 1e-5, BF)
+    rel = (d / 2 + 5) * E
+    assert np.array_equal(q[-3:].cpu().numpy(), codes)
+    _assert_within(sc[-3:], ref_sc[:, 0], rel * ref_sc[:, 0], "scale")
+    _assert_within(y[-3:], v, (rel + E + U) * np.abs(v) * (1 + U), "y")
+    assert not q[:5].any() and not sc[:5].any()
+    del x, q, y
+    k = _module(70001, 16, 32768, 8, seed=92)
+    y = D.dora_linear_i8_fwd(**k)
+    torch.cuda.synchronize()
+    rows = torch.tensor([0, 65535, 65536, 70000], device=DEV)
+    part = {n: (v[rows] if n in ("x_q", "x_scale", "x") else v) for n, v in k.items()}
+    _check_linear(part, y[rows], cols=np.array([0, 127, 128, 20000, 32767]))
+    assert D.dora_device_status() == D.DORA_OK
