@@ -167,7 +167,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
   // without an adapter the launch before may be anything; with one it is P's,
   // which itself came after all others, and only P has to be waited for
-  if (!has_ext) grid_dep_wait();
+  if (!has_ext) {
+    grid_dep_wait();
+    fence_proxy_async_all();
+  }
   grid_dep_launch();
 
   if (warp < 4) {

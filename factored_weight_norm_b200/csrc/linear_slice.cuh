@@ -15,8 +15,9 @@
 // The meeting is what costs beyond the stream: it is done once for the whole
 // tile, by all warps, with the loads from all splits in flight together (in
 // two rounds of 64 tokens by four warps, split after split, 128 tokens took 10
-// of 25 us).  Measured at 8192 x 8192: one token 16.6 us (67 MB streamed in 10 to
-// 11, 6 TB/s or more; 2.5 to the first bytes, 2.5 to join), 128 tokens 21.5.
+// of 25 us).  Measured at 8192 x 8192 without an adapter: one token 15.2 us (67
+// MB streamed in 10, 6 TB/s or more; 2.5 to the first bytes, 2.5 to join; 0.4 for
+// the proxy fence before them), 128 tokens 20.4.
 #pragma once
 
 #include "linear_i8.cuh"
@@ -266,7 +267,10 @@ __global__ void __launch_bounds__(kSlThreads)
     }
     mbar_init(acc_full, 1);
     fence_mbar_init();
-    if (wait_all) grid_dep_wait();
+    if (wait_all) {
+      grid_dep_wait();
+      fence_proxy_async_all();
+    }
     for (int s = 0; s < early; ++s) fill(s, kb0 + s);
   }
   if (warp == 1) {
