@@ -214,14 +214,14 @@ struct RowsI8Args {
   float eps;
 };
 
-// (sum, maximum) over the `warps` warps that meet at barrier `bar`, the same
-// bits in every thread: each warp leaves its own in shared memory and every
-// thread adds them in order (a second round of shuffles would take longer).
+// (sum, maximum) over the CTA's `warps` warps, the same bits in every thread:
+// each warp leaves its own in shared memory and every thread adds them in order
+// (a second round of shuffles would take longer).
 struct RowsI8Shared {
   float sum[32];
   uint32_t top[32];
 };
-__device__ __forceinline__ void rows_i8_reduce(float& sum, uint32_t& top, RowsI8Shared& sh, int warps, int bar) {
+__device__ __forceinline__ void rows_i8_reduce(float& sum, uint32_t& top, RowsI8Shared& sh, int warps) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -230,7 +230,7 @@ __device__ __forceinline__ void rows_i8_reduce(float& sum, uint32_t& top, RowsI8
     sh.sum[warp] = sum;
     sh.top[warp] = top;
   }
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
+  __syncthreads();  // every warp of the CTA; the compiler joins the lanes that the branch above parted
   top = __reduce_max_sync(0xffffffffu, lane < warps ? sh.top[lane] : 0u);
   float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(MAXT) rows_i8_kernel(const RowsI8Args a) {
   row.take(x, r, w, has_res, static_cast<T*>(a.h) + off, col, stride, d);
   float sum = row.sum;
   uint32_t top = __float_as_uint(row.top);
-  rows_i8_reduce(sum, top, sh, blockDim.x >> 5, 0);
+  rows_i8_reduce(sum, top, sh, blockDim.x >> 5);
   const float rstd = HAS_W ? rows_i8_rstd(sum, a.d, a.eps) : 1.f;
   if (threadIdx.x == 0) a.scale[blockIdx.x] = top_scale(top) * rstd;
   row.give(top, top_inverse(top), rstd, a.q + off, a.y ? static_cast<T*>(a.y) + off : nullptr, col, stride, d);
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(1024) rows_i8_long_kernel(const RowsI8Args a) 
     top_f = max_abs<VEC>(top_f, v);
   }
   uint32_t top = __float_as_uint(top_f);
-  rows_i8_reduce(sum, top, sh, blockDim.x >> 5, 0);
+  rows_i8_reduce(sum, top, sh, blockDim.x >> 5);
   const float rstd = w ? rows_i8_rstd(sum, a.d, a.eps) : 1.f;
   const float inv = top_inverse(top);
   if (threadIdx.x == 0) a.scale[row] = top_scale(top) * rstd;
