@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(kSlThreads)
     }
     const bool alive = mbar_wait_warp(acc_full, 0, limit);
     if (!alive && lane == 0) atomicExch(a.status, 5);
+    __syncwarp();
     tc_fence_after();
     if (alive) {
       const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
@@ -397,9 +398,9 @@ __global__ void __launch_bounds__(kSlThreads)
     case 4: slice_join<I8, BN, 4>(a, base_s, rowf, sxs, rank, row0, tok0, ext_any); break;
     default: slice_join<I8, BN, 8>(a, base_s, rowf, sxs, rank, row0, tok0, ext_any); break;
   }
+  __syncwarp();  // the join's loops end at different tokens, and rows, for the lanes of a warp
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kColsTmem);
-  __syncwarp();
   cluster_sync_all();  // no CTA leaves while another reads its exchange area
 }
 
