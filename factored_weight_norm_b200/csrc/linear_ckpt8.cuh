@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const uint32_t ab = it & 1u;
         if (alive && !mbar_wait_warp(&acc_full[ab], (it >> 1) & 1u, limit)) {
           if (lane == 0) lin_timeout(a.status, abort_flag);
+          __syncwarp();
           alive = false;
         }
         if (!alive) continue;

@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       epi_sync();
       if (alive && !mbar_wait_warp(acc_full, it & 1u, limit)) {
         if (lane == 0) lin_timeout(a.status, abort_flag);
+        __syncwarp();
         alive = false;
       }
       if (!alive) continue;
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(base_empty_leader);
+      __syncwarp();
       const int col0 = tn * a.bn + first;
       const float* swg = cf + first;
       const int piece = lane & 3;
