@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
           }
         }
+        __syncwarp();  // rows past the end have parted the lanes; the next load needs them all
       }
       tc_fence_before();
       __syncwarp();

@@ -139,7 +139,7 @@ def test_the_reader_sees_parted_warps():
         assert (not parted_uses(kernel % body)) is ok, body
 
 
-FILES = ("compose.cuh", "quant8.cuh", "ckpt8.cuh", "linear_i8.cuh", "linear_ckpt8.cuh", "linear_slice.cuh")
+FILES = ("compose.cuh", "quant8.cuh", "ckpt8.cuh", "linear_tc.cuh", "linear_i8.cuh", "linear_ckpt8.cuh", "linear_slice.cuh")
 
 
 @pytest.mark.parametrize("name", FILES)
