@@ -194,6 +194,23 @@ __device__ __forceinline__ float round_to(float v, const __nv_bfloat16*) {
 }
 __device__ __forceinline__ float round_to(float v, const float*) { return v; }
 
+// VEC neighbouring values of a row that this kernel may write back in place (h
+// over x or residual): coherent loads, since the non-coherent path holds only
+// for memory that nothing writes while the kernel runs.
+template <typename T, int VEC>
+__device__ __forceinline__ typename VecIO<T, VEC>::Raw ld_row(const T* p) {
+  if constexpr (VEC == 1) {
+    return *p;
+  } else {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+  }
+}
+
 // -------------------------------------------------- rows to codes, with a norm
 // One CTA per row of d columns: h = x + residual in the activation type (the
 // residual stream, written back), then
@@ -329,8 +346,8 @@ __global__ void __launch_bounds__(MAXT) rows_i8_kernel(const RowsI8Args a) {
   for (int i = 0; i < NV; ++i) {
     x[i] = r[i] = w[i] = typename IO::Raw{};
     if (col + i * stride < d) {
-      x[i] = IO::raw(static_cast<const T*>(a.x) + off + col + i * stride);
-      if (has_res) r[i] = IO::raw(static_cast<const T*>(a.residual) + off + col + i * stride);
+      x[i] = ld_row<T, VEC>(static_cast<const T*>(a.x) + off + col + i * stride);
+      if (has_res) r[i] = ld_row<T, VEC>(static_cast<const T*>(a.residual) + off + col + i * stride);
       if (HAS_W) w[i] = IO::raw_param(static_cast<const T*>(a.weight) + col + i * stride);
     }
   }
@@ -359,10 +376,10 @@ __global__ void __launch_bounds__(1024) rows_i8_long_kernel(const RowsI8Args a) 
   for (long long col = static_cast<long long>(threadIdx.x) * VEC; col < a.d;
        col += static_cast<long long>(blockDim.x) * VEC) {
     float v[VEC];
-    VecIO<T, VEC>::load(x + col, v);
+    VecIO<T, VEC>::unpack(ld_row<T, VEC>(x + col), v);
     if (res) {
       float r[VEC];
-      VecIO<T, VEC>::load(res + col, r);
+      VecIO<T, VEC>::unpack(ld_row<T, VEC>(res + col), r);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[e] = round_to(v[e] + r[e], x);
       VecIO<T, VEC>::store(h + col, v);

@@ -265,3 +265,17 @@ def test_workspaces_have_no_token_by_channel_term(lib):
     ws = lib.dora_compose_bwd_ckpt8_workspace_size(8192, 8192)
     assert 0 < ws < 8192 * 8192 / 16 and lib.dora_compose_bwd_ckpt8_workspace_size(65536, 8192) == ws
     assert lib.dora_compose_bwd_ckpt8_workspace_size(-1, 8) == 0
+
+
+def test_rows_written_in_place_are_not_read_through_the_non_coherent_path():
+    # h may be x or residual: in the kernels that write it only the weight, which
+    # nothing writes, may be read as memory that stays as it is
+    import os
+    import re
+
+    with open(os.path.join(build_mod.CSRC, "quant8.cuh")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    rows = text[text.index("struct RowsI8Args"):text.index("void __launch_bounds__(256) dequant_i8_kernel")]
+    reads = re.findall(r"(?:IO|VecIO<T, VEC>)::(?:raw|load)\([^\n]*|__ldg\([^\n]*|ld_stream\w*\([^\n]*|ld\.global\.nc", rows)
+    assert not reads, reads
+    assert "ld.global.nc" not in text[text.index("ld_row(const T* p)"):text.index("struct RowsI8Args")]

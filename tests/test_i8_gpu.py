@@ -515,3 +515,34 @@ def test_offsets_past_32_bits():
     part = {n: (v[rows] if n in ("x_q", "x_scale", "x") else v) for n, v in k.items()}
     _check_linear(part, y[rows], cols=np.array([0, 127, 128, 20000, 32767]))
     assert D.dora_device_status() == D.DORA_OK
+
+
+@pytest.mark.parametrize("rows, cols, dtype", [(300, 4099, F32), (3, 33001, F32), (7, 129, F32), (2, 40000, F32),
+                                               (3, 40000, BF), (400, 2048, BF), (2, 20008, BF)],
+                         ids=lambda v: str(v).replace("torch.", ""))
+@pytest.mark.parametrize("where", ["x", "residual", "both"])
+@pytest.mark.parametrize("norm", [False, True])
+def test_rows_in_place_in_every_layout(rows, cols, dtype, where, norm):
+    # h over x, over residual, and over one tensor that is both: in registers, in
+    # two passes, by vectors and by single values, at row bases off 128 bytes
+    x = _rows(rows, cols, dtype, 101)
+    res = x if where == "both" else _rows(rows, cols, dtype, 102)
+    w = (1 + 0.2 * torch.randn(cols, generator=_gen(103))).to(dtype).to(DEV)
+
+    def call(a, b, h):
+        if norm:
+            return D.dora_rms_norm_i8(a, w, residual=b, h=h, want_y=True)
+        return D.dora_quantize_rows_i8(a, residual=b, h=h)
+
+    ref = call(x, res, None)
+    want_h = (x.float() + res.float()).to(dtype)
+    a = x.clone()
+    b = a if where == "both" else res.clone()
+    got = call(a, b, b if where == "residual" else a)
+    torch.cuda.synchronize()
+    assert torch.equal(ref[2], want_h)
+    assert all(torch.equal(p, q) for p, q in zip(ref, got))
+    v = P.f64(want_h)
+    if norm:
+        v = v * P.f64(w) if dtype == BF else (want_h.cpu().numpy() * w.cpu().numpy()).astype(np.float64)
+    assert np.array_equal(got[0].cpu().numpy(), oracle.encode(v)[0])
