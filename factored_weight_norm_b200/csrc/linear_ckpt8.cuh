@@ -33,6 +33,12 @@ namespace dora {
 
 constexpr int kCkChunk = 6;  // ring stages (of two 64-deep K blocks) summed in TMEM at a time
 
+// First of `steps` K steps that chunk c of `chunks` sums.  The product passes 32
+// bits from 14.7 million input columns on.
+__host__ __device__ __forceinline__ int chunk_start(int steps, int c, int chunks) {
+  return static_cast<int>(static_cast<long long>(steps) * c / chunks);
+}
+
 struct LinearCkptArgs {
   int M, N;
   int kb_main, kb_r;      // K blocks of x W^T and of each half of P B^T
@@ -76,7 +82,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int n_tiles = a.tiles_m * a.tiles_n;
   const int kb_total = a.kb_main + 2 * a.kb_r;
   const int n_stages = (kb_total + kPairKps - 1) / kPairKps;  // per tile
-  const int n_chunks = (n_stages + kCkChunk - 1) / kCkChunk;  // chunk c ends before stage n_stages (c + 1) / n_chunks
+  const int n_chunks = (n_stages + kCkChunk - 1) / kCkChunk;
 
   // bytes that both CTAs' copies bring per stage
   const uint32_t stage_tx = 2 * kPairKps * (kLinABytes + a.bn / 2 * 128u);
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             }
             tc_fence_after();
             const uint32_t d = tmem + ab * kPairBN;
-            const int s0 = n_stages * c / n_chunks, s1 = n_stages * (c + 1) / n_chunks;
+            const int s0 = chunk_start(n_stages, c, n_chunks), s1 = chunk_start(n_stages, c + 1, n_chunks);
             for (int s = s0; s < s1; ++s) {
               if (!mbar_wait(&full[stage], phase, limit)) {
                 lin_timeout(a.status, abort_flag);

@@ -325,3 +325,25 @@ def test_fused_offsets_past_32_bits():
         half = 0.5 * ss.cpu().double().numpy()[:, np.arange(d_out) // 128]
         assert np.all(np.abs(oracle.decode(cc.cpu().numpy(), ss.cpu().numpy(), 128) - z) <= half + 64 * E * (1 + np.abs(z)))
         assert np.all(np.abs(P.f64(yy) - z) <= U * np.abs(z) + 64 * E * (1 + np.abs(z)))
+
+
+def test_fused_forward_over_millions_of_input_columns():
+    # a K of 125,000 steps in 20,834 chunks: their product passes 32 bits.  Operands
+    # of -1, 0 and 1 make every partial sum an integer below 2^24, exact in any
+    # order and under any rounding, and P (below 2^16) exact in two bf16 halves
+    T, K, N, r = 3, 16_000_000, 16, 8
+    g = torch.Generator(device=DEV).manual_seed(15)
+    tri = lambda *k: torch.randint(-1, 2, k, generator=g, device=DEV, dtype=torch.int8).to(BF)  # noqa: E731
+    x, W, A, B = tri(T, K), tri(N, K), tri(r, K), tri(N, r)
+    one = torch.ones(N, device=DEV)
+    y, z8, zs = D.dora_fused_linear_fwd_ckpt8(x, W, A, B, one, one, 1.0)
+    torch.cuda.synchronize()
+    assert D.dora_device_status() == D.DORA_OK
+    xd = x.double()
+    Pm = torch.cat([xd @ A[j:j + 1].double().T for j in range(r)], dim=1)
+    z = torch.cat([xd @ W[j:j + 1].double().T for j in range(N)], dim=1) + Pm @ B.double().T
+    assert Pm.abs().max() < 2 ** 16 and z.abs().max() < 2 ** 24  # of the inputs, not of the kernel
+    codes, sc = oracle.encode(P.f64(z), 128)
+    assert np.array_equal(zs.cpu().numpy(), sc.astype(np.float32))
+    assert np.array_equal(z8.cpu().numpy(), codes)
+    assert torch.equal(y, z.to(BF))
