@@ -1039,6 +1039,9 @@ int launch_p_slice(const void* x, const void* A, __nv_bfloat16* P, __nv_bfloat16
   sa.rows = static_cast<int>(r);
   sa.tokens = static_cast<int>(tokens);
   sa.kb_main = sa.kb_total = static_cast<int>(cdiv(d_in, kLinBK));
+  // P in two halves is wanted as exact as fp32: summed as z is.  One bf16 value
+  // (2^-8) does not show what a single sum drops (1e-5 of it at K = 8192).
+  sa.chunk = P_lo ? kCkChunk * kPairKps : INT32_MAX;
   sa.alpha = s;
   sa.out = P;
   sa.out_lo = P_lo;

@@ -4,15 +4,18 @@
 //   z = x W^T + P B^T,  P = s * x A^T       (the product, before g and b)
 //   y = bf16(g * z + b),  z8, z_scale = 8-bit stretches of 128 columns of z
 //
-// The GEMM is linear_tc.cuh's pair GEMM with two changes that keep z at fp32's
+// The GEMM is linear_tc.cuh's pair GEMM with two changes that keep z near fp32's
 // exactness, since its scales are returned in fp32:
-//  * P = P_hi + P_lo, two bf16 matrices (the extension runs over both); one
-//    alone would move z by 2^-9 of the adapter's share.
+//  * P = P_hi + P_lo, two bf16 matrices (the extension runs over both): off by
+//    at most 2^-16 of P, to either side; one alone would move z by 2^-8 of the
+//    adapter's share.
 //  * The tensor core drops the bits below its accumulator as it adds, always
-//    toward zero: over K = 8192 that took 8.5e-6 of the largest values
-//    (4.0e-6 at 4096).  So K is cut into chunks of at most kCkChunk stages
-//    (768 of K), each summed in TMEM from zero, and the epilogue warps add
-//    the chunks in fp32 registers, which round to nearest.
+//    toward zero: over K = 8192 that took 8.5e-6 of the largest values of
+//    signed operands (4.0e-6 at 4096) and 3.0e-5 of a sum of positive ones.  So
+//    K is cut into chunks of at most kCkChunk stages (768 of K), each summed in
+//    TMEM from zero, and the epilogue warps add the chunks in fp32 registers,
+//    which round to nearest.  P's own sum over K runs in the same chunks
+//    (linear_slice.cuh).
 // Eight epilogue warps hold a 128 x 256 tile in 128 registers a thread; a
 // thread's 128 columns of its row are one stretch, so the maximum and the
 // codes come from registers without any exchange.  Two TMEM accumulators: the
@@ -32,12 +35,6 @@
 namespace dora {
 
 constexpr int kCkChunk = 6;  // ring stages (of two 64-deep K blocks) summed in TMEM at a time
-
-// First of `steps` K steps that chunk c of `chunks` sums.  The product passes 32
-// bits from 14.7 million input columns on.
-__host__ __device__ __forceinline__ int chunk_start(int steps, int c, int chunks) {
-  return static_cast<int>(static_cast<long long>(steps) * c / chunks);
-}
 
 struct LinearCkptArgs {
   int M, N;

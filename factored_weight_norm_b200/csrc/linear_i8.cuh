@@ -30,6 +30,12 @@ constexpr size_t kI8BarrierBytes = 256;
 // per-column epilogue factors of two tiles: sw * g, g, b
 constexpr size_t kI8ColBytes = 2 * 3 * kPairBN * sizeof(float);
 
+// A sum over K in chunks: first of `steps` K steps that chunk c of `chunks` sums.  The product passes 32
+// bits from 14.7 million input columns on.
+__host__ __device__ __forceinline__ int chunk_start(int steps, int c, int chunks) {
+  return static_cast<int>(static_cast<long long>(steps) * c / chunks);
+}
+
 struct LinearI8Args {
   int M, N;              // tokens and output channels
   int kb_main, kb_total; // K blocks of the int8 operands; total with the adapter's

@@ -47,6 +47,7 @@ struct SliceArgs {
   const float* m;
   const float* n;
   const __nv_bfloat16* bias;
+  int chunk;              // !I8: K blocks that one TMEM sum takes at most
   float alpha;            // !I8: scale of the product
   __nv_bfloat16* out;     // [tokens, rows]
   __nv_bfloat16* out_lo;  // !I8: what the output's rounding leaves, or null
@@ -212,14 +213,17 @@ __global__ void __launch_bounds__(kDownThreads) down_tokens_kernel(const __nv_bf
 }
 
 // I8: out = bf16(b + g * (sx sw * (W_q x_q^T) + B P^T)), tmW/tmX int8 and
-// tmB/tmP the adapter's; else out = bf16(alpha * W x^T), all bf16.
+// tmB/tmP the adapter's; else out = bf16(alpha * W x^T), all bf16, whose sum over
+// K runs in chunks of a.chunk blocks: each in one of two TMEM accumulators, added
+// by the epilogue warps in fp32 registers while the next one is summed.  (The
+// tensor core drops bits toward zero as it adds; one chunk is the plain sum.)
 template <bool I8, int BN>
-__global__ void __launch_bounds__(kSlThreads)
+__global__ void __launch_bounds__(kSlThreads, 2)
     linear_slice_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmP,
                         const SliceArgs a) {
   constexpr uint32_t kStageBytes = slice_stage_bytes(BN);
-  constexpr uint32_t kColsTmem = I8 ? 2 * BN : (BN < 32 ? 32 : BN);
+  constexpr uint32_t kColsTmem = 2 * BN;  // I8: the base and the adapter; else two chunks
   const int stages = a.stages;  // the host's: the exchange fits in the ring
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
@@ -229,8 +233,9 @@ __global__ void __launch_bounds__(kSlThreads)
   float* sxs = rowf + 3 * kLinBM;                                        // the tokens' scales
   uint64_t* full = reinterpret_cast<uint64_t*>(sxs + 128);
   uint64_t* empty = full + stages;
-  uint64_t* acc_full = empty + stages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  uint64_t* acc_full = empty + stages;  // [2], I8 uses one
+  uint64_t* acc_empty = acc_full + 2;   // [2], for chunks
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -244,6 +249,7 @@ __global__ void __launch_bounds__(kSlThreads)
   const int kb0 = slice_start(a, static_cast<int>(rank), static_cast<int>(splits));
   const int kb1 = slice_start(a, static_cast<int>(rank) + 1, static_cast<int>(splits));
   const bool has_ext = I8 && kb1 > a.kb_main;
+  const int n_chunks = I8 ? 1 : (kb1 - kb0 - 1) / a.chunk + 1;
   const long long limit = a.wait_limit;
 
   // K block kb into a stage of the ring
@@ -265,7 +271,10 @@ __global__ void __launch_bounds__(kSlThreads)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(acc_full, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4);  // the epilogue warps
+    }
     fence_mbar_init();
     if (wait_all) {
       grid_dep_wait();
@@ -317,36 +326,45 @@ __global__ void __launch_bounds__(kSlThreads)
       bool ok = true;
       int stage = 0;
       uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&full[stage], phase, limit)) {
+      for (int c = 0; c < n_chunks && ok; ++c) {
+        const int c0 = kb0 + chunk_start(kb1 - kb0, c, n_chunks), c1 = kb0 + chunk_start(kb1 - kb0, c + 1, n_chunks);
+        const uint32_t d = tmem + (c & 1) * BN;
+        if (!I8 && !mbar_wait(&acc_empty[c & 1], ((c >> 1) & 1u) ^ 1u, limit)) {
           atomicExch(a.status, 5);
           ok = false;
-          break;
         }
-        tc_fence_after();
-        const uint64_t ad = desc0 + static_cast<uint64_t>(stage) * (kStageBytes >> 4);
-        const uint64_t bd = ad + (kLinABytes >> 4);
-        const bool ext = I8 && kb >= a.kb_main;
-        const uint32_t first = ext ? a.kb_main : kb0;
+        if (!I8) tc_fence_after();
+        for (int kb = c0; kb < c1 && ok; ++kb) {
+          if (!mbar_wait(&full[stage], phase, limit)) {
+            atomicExch(a.status, 5);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = desc0 + static_cast<uint64_t>(stage) * (kStageBytes >> 4);
+          const uint64_t bd = ad + (kLinABytes >> 4);
+          const bool ext = I8 && kb >= a.kb_main;
+          const int first = ext ? a.kb_main : c0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t acc = (kb > static_cast<int>(first) || k > 0) ? 1u : 0u;
-          if (ext)
-            mma_bf16(tmem + BN, ad + 2 * k, bd + 2 * k, idesc_e, acc);
-          else if (I8)
-            mma_i8(tmem, ad + 2 * k, bd + 2 * k, idesc_m, acc);
-          else
-            mma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc_m, acc);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t acc = (kb > first || k > 0) ? 1u : 0u;
+            if (ext)
+              mma_bf16(tmem + BN, ad + 2 * k, bd + 2 * k, idesc_e, acc);
+            else if (I8)
+              mma_i8(tmem, ad + 2 * k, bd + 2 * k, idesc_m, acc);
+            else
+              mma_bf16(d, ad + 2 * k, bd + 2 * k, idesc_m, acc);
+          }
+          mma_commit(&empty[stage]);
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        mma_commit(&empty[stage]);
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        // after a wait that gave up the MMAs already issued must still end before TMEM is freed
+        mma_commit(&acc_full[c & 1]);
+        if (!ok) mbar_wait(&acc_full[c & 1], (c >> 1) & 1u, limit);
       }
-      // after a wait that gave up the MMAs already issued must still end before TMEM is freed
-      mma_commit(acc_full);
-      if (!ok) mbar_wait(acc_full, 0, limit);
     }
   }
   __syncwarp();
@@ -367,14 +385,43 @@ __global__ void __launch_bounds__(kSlThreads)
       rowf[kLinBM + et] = g;
       rowf[2 * kLinBM + et] = b;
       if (et < BN) sxs[et] = tok0 + et < a.tokens ? __ldg(a.x_scale + tok0 + et) : 0.f;
+      __syncwarp();
     }
-    const bool alive = mbar_wait_warp(acc_full, 0, limit);
-    if (!alive && lane == 0) atomicExch(a.status, 5);
-    __syncwarp();
-    tc_fence_after();
-    if (alive) {
-      const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(smem) + q * 32 + lane;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(smem) + q * 32 + lane;
+    bool alive = true;
+    float v[I8 ? 1 : BN];  // !I8: the chunks' sum
+    if (!I8) {
+#pragma unroll
+      for (int e = 0; e < BN; ++e) v[I8 ? 0 : e] = 0.f;
+    }
+#pragma unroll 1
+    for (int c = 0; c < n_chunks && alive; ++c) {
+      if (!mbar_wait_warp(&acc_full[c & 1], (c >> 1) & 1u, limit)) {
+        if (lane == 0) atomicExch(a.status, 5);
+        __syncwarp();
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      if (!I8) {
+#pragma unroll
+        for (int j = 0; j < BN; j += 16) {
+          if (tok0 + j < a.tokens) {  // warp-uniform
+            uint32_t u[16];
+            tmem_ld16(lane_addr + (c & 1) * BN + j, u);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[I8 ? 0 : j + e] += __uint_as_float(u[e]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[c & 1]);
+        __syncwarp();
+      }
+    }
+    // every MMA has ended: the ring is free
+    if (alive && I8) {
 #pragma unroll 4
       for (int j = 0; j < BN; j += 16) {
         if (tok0 + j >= a.tokens) break;  // warp-uniform
@@ -388,7 +435,12 @@ __global__ void __launch_bounds__(kSlThreads)
           for (int e = 0; e < 16; ++e) dst[(BN + j + e) * 128] = u[e];
         }
       }
+    } else if (alive) {
+#pragma unroll
+      for (int e = 0; e < BN; ++e)
+        if (tok0 + e < a.tokens) dst[e * 128] = __float_as_uint(v[I8 ? 0 : e]);
     }
+    __syncwarp();
   }
   tc_fence_before();
   cluster_sync_all();

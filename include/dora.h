@@ -406,9 +406,10 @@ DORA_API size_t dora_fused_linear_fwd_ckpt8_workspace_size(int64_t tokens, int64
 
 /* dora_fused_linear_fwd that also keeps z = x W^T + s (x A^T) B^T in 8 bits, as
  * dora_compose_fwd_ckpt8 does (z in fp32, before g and b): the fused forward
- * writes neither activation, so this is its training form.  P is kept in two
- * bf16 halves and z summed in fp32 over chunks of K, so y and the scales are
- * those of an fp32 product (y's last rounding apart).  z8 16-byte aligned;
+ * writes neither activation, so this is its training form.  P and z are
+ * both summed in fp32 over chunks of K, and P is kept in two bf16 halves (off by
+ * at most 2^-16 of itself), so the scales and y before its last rounding are an
+ * fp32 product's but for that part of the adapter's share.  z8 16-byte aligned;
  * workspace at least dora_fused_linear_fwd_ckpt8_workspace_size() bytes; the
  * rest as there. */
 DORA_API int dora_fused_linear_fwd_ckpt8(const void* x, const void* W, const void* A, const void* B, const void* bias,

@@ -347,3 +347,52 @@ def test_fused_forward_over_millions_of_input_columns():
     assert np.array_equal(zs.cpu().numpy(), sc.astype(np.float32))
     assert np.array_equal(z8.cpu().numpy(), codes)
     assert torch.equal(y, z.to(BF))
+
+
+def _scale_bias(T, K, N, r, adapter):
+    """Mean relative error of the scales of z for positive operands: the tensor
+    core's truncation always goes down, rounding to nearest goes both ways.  With
+    ``adapter`` the base weight is zero and B picks one rank a channel, so z is P."""
+    g = torch.Generator(device=DEV).manual_seed(16)
+    x = torch.rand(T, K, generator=g, device=DEV).to(BF)
+    one = torch.ones(N, device=DEV)
+    if adapter:
+        W = torch.zeros(N, K, dtype=BF, device=DEV)
+        A = torch.rand(r, K, generator=g, device=DEV).to(BF)
+        B = torch.zeros(N, r, dtype=BF, device=DEV)
+        B[torch.arange(N), torch.arange(N) % r] = 1
+        z = (x.double() @ A.double().T).repeat(1, -(-N // r))[:, :N]
+    else:
+        W = torch.rand(N, K, generator=g, device=DEV).to(BF)
+        A, B = torch.zeros(r, K, dtype=BF, device=DEV), torch.zeros(N, r, dtype=BF, device=DEV)
+        z = x.double() @ W.double().T
+    _, _, zs = D.dora_fused_linear_fwd_ckpt8(x, W, A, B, one, one, 1.0)
+    top = torch.stack([z[:, j:j + 128].abs().amax(dim=1) for j in range(0, N, 128)], dim=1)
+    torch.cuda.synchronize()
+    assert D.dora_device_status() == D.DORA_OK
+    return ((127 * zs.double() - top) / top).mean().item()
+
+
+# A chunk is at most 768 of K: 48 additions of 16 products, and addition i of a
+# growing sum drops less than 2^-23 of i / 48 of it, 24.5 * 2^-23 in all.  The 11
+# chunks of K = 8192 are added with rounding (each 2^-24 of what is there so far,
+# 6 * 2^-24 in all), and the scale takes two more roundings.
+CHUNK_BIAS = 24.5 * 2.0 ** -23 + 6 * E + 2 * E
+
+
+def test_scales_of_a_long_k_are_not_low():
+    # one sum over 4096 of K would be 5e-6 low, over all 8192 1e-5
+    bias = _scale_bias(256, 8192, 384, 0, False)
+    assert abs(bias) <= CHUNK_BIAS, bias
+
+
+@pytest.mark.parametrize("T, N, r", [(512, 8192, 384),   # P beside the product, K in one piece
+                                     (6400, 256, 384),   # many tokens, K in one piece
+                                     (140, 384, 128),    # K in eighths
+                                     (40, 264, 72), (20, 264, 8), (7, 128, 8)])  # narrower token tiles
+def test_scales_of_an_adapter_s_long_k_are_not_low(T, N, r):
+    # z is P alone.  Its low half rounds by at most 2^-16 of P either way: over the
+    # T rows and r / 128 distinct stretches that leaves six times 2^-16 over the
+    # root of their number
+    bias = _scale_bias(T, 8192, N, r, True)
+    assert abs(bias) <= CHUNK_BIAS + 2 * E + 6 * U * U / (T * max(1, r // 128)) ** 0.5, bias
