@@ -82,6 +82,20 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t
       : "memory");
 }
 
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// v = hi + lo: returns hi, a bf16 value, and what that leaves.  A finite v past
+// bf16's largest number keeps that one (v may round to infinity, and the rest
+// would be minus infinity); of an infinity nothing is left (and not NaN).
+__device__ __forceinline__ float split_bf16(float v, float& lo) {
+  constexpr float kBf16Max = 255.f * 0x1p120f, kInf = __builtin_huge_valf();
+  const float hi = __bfloat162float(__float2bfloat16_rn(fabsf(v) < kInf ? fminf(fmaxf(v, -kBf16Max), kBf16Max) : v));
+  lo = fabsf(v) == kInf ? 0.f : v - hi;
+  return hi;
+}
+
 // One thread's share of the joined tile: eight rows (from `group`) of every
 // token j with j % S == rank that falls to it, from the S splits' exchange
 // areas ([token][128 rows] words; the adapter's behind them in the last one).
@@ -144,21 +158,14 @@ __device__ __forceinline__ void slice_join(const SliceArgs& a, uint32_t area, co
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] *= a.alpha;
     }
-    uint4 pk;
-    pk.x = pack_bf16x2(o[0], o[1]);
-    pk.y = pack_bf16x2(o[2], o[3]);
-    pk.z = pack_bf16x2(o[4], o[5]);
-    pk.w = pack_bf16x2(o[6], o[7]);
     const long long off = static_cast<long long>(t) * a.rows + row0 + group;
-    *reinterpret_cast<uint4*>(a.out + off) = pk;
     if (!I8 && a.out_lo) {
-      uint4 lo;
-      lo.x = pack_bf16x2(o[0] - bf16_lo(pk.x), o[1] - bf16_hi(pk.x));
-      lo.y = pack_bf16x2(o[2] - bf16_lo(pk.y), o[3] - bf16_hi(pk.y));
-      lo.z = pack_bf16x2(o[4] - bf16_lo(pk.z), o[5] - bf16_hi(pk.z));
-      lo.w = pack_bf16x2(o[6] - bf16_lo(pk.w), o[7] - bf16_hi(pk.w));
-      *reinterpret_cast<uint4*>(a.out_lo + off) = lo;
+      float rest[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = split_bf16(o[e], rest[e]);
+      *reinterpret_cast<uint4*>(a.out_lo + off) = pack_bf16x8(rest);
     }
+    *reinterpret_cast<uint4*>(a.out + off) = pack_bf16x8(o);
   }
 }
 

@@ -406,12 +406,13 @@ DORA_API size_t dora_fused_linear_fwd_ckpt8_workspace_size(int64_t tokens, int64
 
 /* dora_fused_linear_fwd that also keeps z = x W^T + s (x A^T) B^T in 8 bits, as
  * dora_compose_fwd_ckpt8 does (z in fp32, before g and b): the fused forward
- * writes neither activation, so this is its training form.  P and z are
- * both summed in fp32 over chunks of K, and P is kept in two bf16 halves (off by
- * at most 2^-16 of itself), so the scales and y before its last rounding are an
- * fp32 product's but for that part of the adapter's share.  z8 16-byte aligned;
- * workspace at least dora_fused_linear_fwd_ckpt8_workspace_size() bytes; the
- * rest as there. */
+ * writes neither activation, so this is its training form.  P and z are both
+ * summed in fp32 over chunks of K, and P is kept in two bf16 halves (off by at
+ * most 2^-16 of itself), so the scales and y before its last rounding are an
+ * fp32 product's but for that part of the adapter's share.  An infinity or a NaN
+ * makes the y that it makes there (an infinity in B may make NaN instead).  z8
+ * 16-byte aligned; workspace at least
+ * dora_fused_linear_fwd_ckpt8_workspace_size() bytes; the rest as there. */
 DORA_API int dora_fused_linear_fwd_ckpt8(const void* x, const void* W, const void* A, const void* B, const void* bias,
                                          const float* m, const float* n, float s, int64_t tokens, int64_t d_in,
                                          int64_t d_out, int64_t r, dora_dtype dt, void* y, int8_t* z8, float* z_scale,

@@ -396,3 +396,45 @@ def test_scales_of_an_adapter_s_long_k_are_not_low(T, N, r):
     # root of their number
     bias = _scale_bias(T, 8192, N, r, True)
     assert abs(bias) <= CHUNK_BIAS + 2 * E + 6 * U * U / (T * max(1, r // 128)) ** 0.5, bias
+
+
+@pytest.mark.parametrize("T, N", [(9, 264), (300, 264), (300, 1000)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_fused_rows_that_are_zero_or_not_finite(T, N, bias):
+    # positive weights, so that an infinite input makes every channel +inf and not a difference of infinities
+    K, r = 136, 24
+    g = _gen(17)
+    rand = lambda *k: (0.1 + torch.rand(*k, generator=g)).to(BF).to(DEV)  # noqa: E731
+    x, W, A, B = rand(T, K), rand(N, K), rand(r, K), rand(N, r)
+    x[0] = 0
+    x[1, 5] = float("inf")
+    x[2, 100] = float("nan")
+    x[3] = 2.0 ** -122            # a stretch below 2^-100
+    x[4, 7] = -float("inf")
+    # P rounds to infinity in bf16 alone: 255.75 / 256 of 2^128 (B takes it back)
+    x[5] = 0
+    x[5, 0], x[5, 1] = 255 * 2.0 ** 120, 2.0 ** 118
+    A[:, 0], A[:, 1] = 1.0, 3.0
+    W[:, 0], W[:, 1] = 2.0 ** -20, 2.0 ** -20
+    B *= 2.0 ** -12
+    m = (1 + 0.1 * torch.rand(N, generator=g)).to(DEV)
+    b = rand(N) if bias else None
+    y, z8, zs = D.dora_fused_linear_fwd_ckpt8(x, W, A, B, m, torch.ones(N, device=DEV), 1.0, bias=b)
+    dy = rand(T, N)
+    d_base, d_lora, d_m = D.dora_compose_bwd_ckpt8(dy, z8, zs, m, torch.ones(N, device=DEV), 1.0)
+    torch.cuda.synchronize()
+    assert D.dora_device_status() == D.DORA_OK
+    assert torch.equal(y[0], torch.zeros(N, dtype=BF, device=DEV) if b is None else b)
+    plain = D.dora_fused_linear_fwd(x, W, A, B, m, torch.ones(N, device=DEV), 1.0, bias=b)
+    assert torch.equal(y[[1, 2, 4]].nan_to_num(7.0), plain[[1, 2, 4]].nan_to_num(7.0))
+    assert not z8[[0, 3]].any() and not zs[[0, 3]].any()
+    assert (y[1] == float("inf")).all() and torch.isnan(y[2]).all() and (y[4] == -float("inf")).all()
+    assert torch.isnan(zs[[1, 2, 4]]).all() and not z8[[1, 2, 4]].any()
+    rest = torch.tensor([i for i in range(T) if i not in (1, 2, 4)], device=DEV)
+    z = P.f64(x[rest]) @ P.f64(W).T + (P.f64(x[rest]) @ P.f64(A).T) @ P.f64(B).T
+    want = P.f64(m) * z + (0.0 if b is None else P.f64(b))
+    # positive sums of K + r terms in fp32, P in two halves, one bf16 rounding
+    rel = (2 * K + r + 16) * E + U * U
+    assert np.all(np.abs(P.f64(y[rest]) - want) <= (rel + U) * np.abs(want) * (1 + U))
+    assert torch.isfinite(zs[rest]).all() and torch.isnan(d_m).all()
+    assert torch.isfinite(d_base).all() and torch.isfinite(d_lora).all()
