@@ -261,11 +261,18 @@ __device__ __forceinline__ void rows_i8_reduce(float& sum, uint32_t& top, RowsI8
   sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
 }
 
-// The row's factor 1 / sqrt(mean + eps); NaN where the squares left fp32's
-// range, so that the row does not come back as zeros.
-__device__ __forceinline__ float rows_i8_rstd(float sum, long long d, float eps) {
-  const float ms = sum / static_cast<float>(d);
-  return ms < __uint_as_float(kTopInf) ? 1.f / sqrtf(ms + eps) : __uint_as_float(0x7FC00000u);
+// The row's factor 1 / sqrt(mean + eps); NaN where the squares left fp32's range,
+// so that the row comes back neither as zeros nor as infinities: their sum past
+// it, or mean + eps below its normal numbers (an eps of zero, or nearly, and
+// values below 2^-63 or so).  A row of zeros (top, its largest |h * w|, is zero)
+// stays zeros whatever eps.
+__device__ __forceinline__ float rows_i8_rstd(float sum, uint32_t top, long long d, float eps) {
+  const float ms = sum / static_cast<float>(d), t = ms + eps;
+  if (ms < __uint_as_float(kTopInf)) {
+    if (t >= 0x1p-126f) return 1.f / sqrtf(t);
+    if (top == 0u) return 1.f;
+  }
+  return __uint_as_float(0x7FC00000u);
 }
 
 // One row in a thread's registers: NV vectors of VEC columns, `stride` columns
@@ -356,7 +363,7 @@ __global__ void __launch_bounds__(MAXT) rows_i8_kernel(const RowsI8Args a) {
   float sum = row.sum;
   uint32_t top = __float_as_uint(row.top);
   rows_i8_reduce(sum, top, sh, blockDim.x >> 5);
-  const float rstd = HAS_W ? rows_i8_rstd(sum, a.d, a.eps) : 1.f;
+  const float rstd = HAS_W ? rows_i8_rstd(sum, top, a.d, a.eps) : 1.f;
   if (threadIdx.x == 0) a.scale[blockIdx.x] = top_scale(top) * rstd;
   row.give(top, top_inverse(top), rstd, a.q + off, a.y ? static_cast<T*>(a.y) + off : nullptr, col, stride, d);
 }
@@ -397,7 +404,7 @@ __global__ void __launch_bounds__(1024) rows_i8_long_kernel(const RowsI8Args a) 
   }
   uint32_t top = __float_as_uint(top_f);
   rows_i8_reduce(sum, top, sh, blockDim.x >> 5);
-  const float rstd = w ? rows_i8_rstd(sum, a.d, a.eps) : 1.f;
+  const float rstd = w ? rows_i8_rstd(sum, top, a.d, a.eps) : 1.f;
   const float inv = top_inverse(top);
   if (threadIdx.x == 0) a.scale[row] = top_scale(top) * rstd;
   for (long long col = static_cast<long long>(threadIdx.x) * VEC; col < a.d;

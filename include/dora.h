@@ -348,8 +348,10 @@ DORA_API int dora_quantize_rows_i8(const void* x, const void* residual, int64_t 
  *
  * fp32 arithmetic; the codes come from h * weight alone (rstd is one factor of
  * a row's values and enters its scale only).  weight: [d] in dt.  eps >= 0.  A
- * row whose mean square leaves fp32's range gets the scale NaN.  Shapes,
- * alignment and errors as dora_quantize_rows_i8. */
+ * row gets the scale NaN, and y NaN, where fp32 does not hold its norm: the sum
+ * of its squares overflows, or mean(h^2) + eps is below 2^-126 and h * weight is
+ * not zero everywhere (where it is, the scale and y are 0).  Shapes, alignment
+ * and errors as dora_quantize_rows_i8. */
 DORA_API int dora_rms_norm_i8(const void* x, const void* residual, const void* weight, float eps, int64_t tokens,
                               int64_t d, dora_dtype dt, void* h, void* y, int8_t* q, float* scale, void* stream);
 

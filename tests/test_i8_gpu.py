@@ -546,3 +546,34 @@ def test_rows_in_place_in_every_layout(rows, cols, dtype, where, norm):
     if norm:
         v = v * P.f64(w) if dtype == BF else (want_h.cpu().numpy() * w.cpu().numpy()).astype(np.float64)
     assert np.array_equal(got[0].cpu().numpy(), oracle.encode(v)[0])
+
+
+@pytest.mark.parametrize("dtype, cols", [(BF, 264), (F32, 1024), (F32, 4099), (BF, 40000), (F32, 33001)])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-30])
+def test_rms_norm_of_rows_near_zero(dtype, cols, eps):
+    # the factor 1 / sqrt(mean + eps) where the squares leave fp32's normal range:
+    # a zero row gives zeros, a row whose mean square is too small for fp32 gives
+    # NaN and not infinities, and the smallest that is not keeps its values
+    x = torch.zeros(6, cols)
+    x[1] = 2.0 ** -80 * (1 + torch.arange(cols) % 3)  # squares below the smallest subnormal
+    x[2] = 2.0 ** -73                                  # squares of one subnormal step's size
+    x[3] = 2.0 ** -62 * (1 + torch.arange(cols) % 5)   # mean square above 2^-124
+    x[4] = torch.randn(cols, generator=_gen(111))
+    x[5, 0] = 2.0 ** -20                               # one value in a row of zeros
+    x = x.to(dtype).to(DEV)
+    w = (1 + 0.2 * torch.rand(cols, generator=_gen(112))).to(dtype).to(DEV)
+    eps32 = float(np.float32(eps))
+    q, scale, _, y = D.dora_rms_norm_i8(x, w, eps, want_y=True)
+    v = D.dora_dequantize_i8(q, scale, dtype=F32)
+    torch.cuda.synchronize()
+    assert scale[0] == 0 and not y[0].any() and not v[0].any()
+    with np.errstate(divide="ignore", invalid="ignore"):  # the zero row's own factor
+        codes, sc, want = _norm_reference(x, w, eps32, dtype)
+    kept = [3, 4, 5] if eps < 1e-40 else [1, 2, 3, 4, 5]
+    for i in (1, 2):
+        if i not in kept:
+            assert torch.isnan(scale[i]) and torch.isnan(y[i]).all() and torch.isnan(v[i]).all()
+    rel = (cols / 2 + 6) * E  # as above; each square's own rounding may be 2^-150, 2^-24 of 2^-126
+    assert np.array_equal(q[kept].cpu().numpy(), codes[kept])
+    _assert_within(scale[kept], sc[kept, 0], rel * sc[kept, 0], "scale")
+    _assert_within(y[kept], want[kept], (rel + E + (U if dtype == BF else 0)) * np.abs(want[kept]) * (1 + U), "y")
