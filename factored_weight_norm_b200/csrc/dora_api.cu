@@ -1199,8 +1199,10 @@ int launch_rows_i8(const RowsI8Args& a, const DeviceInfo* dev, cudaStream_t st) 
   if (cdiv(a.d, 8) <= most) return launch_after(rows_i8_kernel<T, VEC, 8 / VEC, 1024, HAS_W>, grid, threads(8 / VEC), st, a);
   if (cdiv(a.d, 16) <= most)
     return launch_after(rows_i8_kernel<T, VEC, 16 / VEC, 1024, HAS_W>, grid, threads(16 / VEC), st, a);
-  if (cdiv(a.d, 32) <= 256)
-    return launch_after(rows_i8_kernel<T, VEC, 32 / VEC, 256, HAS_W>, grid, threads(32 / VEC), st, a);
+  if constexpr (VEC > 1) {  // single values take 16 columns a thread up to 16384
+    if (cdiv(a.d, 32) <= 256)
+      return launch_after(rows_i8_kernel<T, VEC, 32 / VEC, 256, HAS_W>, grid, threads(32 / VEC), st, a);
+  }
   if (cdiv(a.d, 32) <= 1024)
     return launch_after(rows_i8_kernel<T, VEC, 32 / VEC, 1024, HAS_W>, grid, threads(32 / VEC), st, a);
   return launch_after(rows_i8_long_kernel<T, VEC>, grid, 1024, st, a);
