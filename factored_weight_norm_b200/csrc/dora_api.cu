@@ -1083,12 +1083,10 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
   __nv_bfloat16* P = static_cast<__nv_bfloat16*>(workspace);
 
   // B-side boxes hold the bn / 2 rows one CTA of a pair owns
-  const int bn_p = r > 0 ? pick_bn(r) : 256, bn_y = ckpt ? pick_bn_waves(cdiv(tokens, kPairBM), d_out, dev) : pick_bn(d_out);
-  CUtensorMap tmX, tmW, tmA, tmP, tmB;
+  const int bn_y = ckpt ? pick_bn_waves(cdiv(tokens, kPairBM), d_out, dev) : pick_bn(d_out);
+  CUtensorMap tmX, tmW, tmP, tmB;
   if (make_map(&tmX, x, tokens, d_in) || make_map(&tmW, W, d_out, d_in, bn_y / 2)) return DORA_ERR_CUDA;
-  if (r > 0 && (make_map(&tmA, A, r, d_in, bn_p / 2) || make_map(&tmP, P, tokens, r) ||
-                make_map(&tmB, B, d_out, r, bn_y / 2)))
-    return DORA_ERR_CUDA;
+  if (r > 0 && (make_map(&tmP, P, tokens, r) || make_map(&tmB, B, d_out, r, bn_y / 2))) return DORA_ERR_CUDA;
   const int kb_main = static_cast<int>(cdiv(d_in, kLinBK));
   const int stages = linear_pair_stages(dev->smem_optin);
   if (stages < 2) return DORA_ERR_UNSUPPORTED;
@@ -1126,7 +1124,9 @@ int fused_linear(const void* x, const void* W, const void* A, const void* B, con
     return launch_error();
   }
 
-  if (r > 0 && launch_p(tmX, tmA, P, s, tokens, d_in, r, dev, st)) return DORA_ERR_CUDA;
+  CUtensorMap tmA;
+  if (r > 0 && (make_map(&tmA, A, r, d_in, pick_bn(r) / 2) || launch_p(tmX, tmA, P, s, tokens, d_in, r, dev, st)))
+    return DORA_ERR_CUDA;
   // 2) y = bf16(g * [x | P] [W | B]^T + b), dependent on 1) only for the extension blocks
   LinearArgs la{};
   la.M = static_cast<int>(tokens);
