@@ -438,3 +438,30 @@ def test_fused_rows_that_are_zero_or_not_finite(T, N, bias):
     assert np.all(np.abs(P.f64(y[rest]) - want) <= (rel + U) * np.abs(want) * (1 + U))
     assert torch.isfinite(zs[rest]).all() and torch.isnan(d_m).all()
     assert torch.isfinite(d_base).all() and torch.isfinite(d_lora).all()
+
+
+def test_two_graphs_share_a_workspace():
+    # two captured backwards of different shapes and one eager call take turns on one workspace
+    shapes = [(700, 520, BF), (260, 1100, F32)]
+    size = max(D.dora_compose_bwd_ckpt8_workspace_size(T, d) for T, d, _ in shapes)
+    ws = torch.randint(0, 256, (size,), dtype=torch.uint8, device=DEV)
+    runs = []
+    for i, (T, d, dtype) in enumerate(shapes):
+        base, lora, m, n, _, dy = _acts(T, d, dtype, False, seed=20 + i)
+        _, z8, zs = D.dora_compose_fwd_ckpt8(base, lora, m, n, 0.5)
+        ref = D.dora_compose_bwd_ckpt8(dy, z8, zs, m, n, 0.5)
+        out = [torch.empty_like(t) for t in ref]
+        call = lambda a=(dy, z8, zs, m, n, 0.5), o=out: D.dora_compose_bwd_ckpt8(*a, *o, workspace=ws)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        runs.append((graph, call, out, ref))
+    for turn in range(6):
+        for graph, call, out, ref in runs if turn % 2 else runs[::-1]:
+            for t in out:
+                t.fill_(7.0)
+            call() if turn == 3 else graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, ref)), turn

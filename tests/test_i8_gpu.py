@@ -577,3 +577,44 @@ def test_rms_norm_of_rows_near_zero(dtype, cols, eps):
     assert np.array_equal(q[kept].cpu().numpy(), codes[kept])
     _assert_within(scale[kept], sc[kept, 0], rel * sc[kept, 0], "scale")
     _assert_within(y[kept], want[kept], (rel + E + (U if dtype == BF else 0)) * np.abs(want[kept]) * (1 + U), "y")
+
+
+@pytest.mark.parametrize("d_in, d_out", [(528, 264), (4112, 1000)])
+@pytest.mark.parametrize("bias, mag", [(True, True), (False, False)])
+def test_without_an_adapter_a_token_does_not_depend_on_its_batch(d_in, d_out, bias, mag):
+    # every token tile of the slices, and the pair product on both sides of their
+    # border: the int32 sums are exact and the epilogues the same operations
+    k = _module(300, d_in, d_out, 0, bias=bias, mag=mag, seed=121)
+    y = D.dora_linear_i8_fwd(**k)
+    for T in (1, 3, 16, 17, 32, 33, 64, 65, 127, 128, 129, 256, 257):
+        part = {**k, "x_q": k["x_q"][:T], "x_scale": k["x_scale"][:T]}
+        assert torch.equal(D.dora_linear_i8_fwd(**part), y[:T]), T
+    torch.cuda.synchronize()
+    assert D.dora_device_status() == D.DORA_OK
+    _check_linear(k, y)
+
+
+@pytest.mark.parametrize("T", [2, 40, 200])
+def test_serving_a_module_with_the_norm_of_its_codes(T):
+    # the weight's codes, n from the weight that they stand for, a norm's codes, the product
+    d_in, d_out, r, s = 1024, 520, 32, 0.5
+    g = _gen(131)
+    rn = lambda *k: torch.randn(*k, generator=g)  # noqa: E731
+    W = (0.02 * rn(d_out, d_in)).to(BF).to(DEV)
+    A = ((2 * torch.rand(r, d_in, generator=g) - 1) / d_in ** 0.5).to(BF).to(DEV)
+    B = (0.05 * rn(d_out, r)).to(BF).to(DEV)
+    m = (0.6 + 0.1 * torch.rand(d_out, generator=g)).to(DEV)
+    W_q, w_scale, _ = D.dora_quantize_rows_i8(W)
+    n = D.dora_factored_norm(D.dora_dequantize_i8(W_q, w_scale), A, B, s)
+    x = _rows(T, d_in, BF, 132)
+    q, scale, _, y = D.dora_rms_norm_i8(x, torch.ones(d_in, dtype=BF, device=DEV), 1e-6, want_y=True)
+    k = dict(x_q=q, x_scale=scale, W_q=W_q, w_scale=w_scale, x=y, A=A, B=B, m=m, n=n, s=s)
+    out = D.dora_linear_i8_fwd(**k)
+    torch.cuda.synchronize()
+    _check_linear(k, out)
+    # n is the norm of codes * scale + s B A: its rounding to bf16 moves the weight by
+    # U of itself at most, and with it the norm; the norm's own tolerance comes on top
+    kept = oracle.decode(W_q.cpu().numpy(), w_scale.cpu().numpy())
+    exact = oracle.row_norm(kept, P.f64(A), P.f64(B), s)
+    slack = U * np.linalg.norm(kept, axis=1) + P.NORM_RTOL_BF16 * exact
+    assert np.all(np.abs(P.f64(n) - exact) <= slack)
