@@ -965,12 +965,19 @@ int launch_p(const CUtensorMap& tmX, const CUtensorMap& tmA, __nv_bfloat16* P, f
              : DORA_ERR_CUDA;
 }
 
-// Up to this many tokens the int8 linear runs on slices of the weight.
+// Up to this many tokens the int8 linear runs on slices of the weight (8192 x
+// 8192 without an adapter: 65 tokens 19.5 us, 23.9 on pairs; 128 tokens 21.1 and
+// 24.2; 129 tokens 32.0 on two token tiles of slices, 24.4 on pairs; 4096 x 4096:
+// 9.5 and 12.9, 11.4 and 13.1, 12.9 and 13.3).  The rule looks at the tokens
+// alone: beside an adapter of rank 384 the pairs are ahead from 65 tokens on
+// (8192 x 8192: 35.6 us on slices, 31.1 on pairs; 128 tokens 39.9 and 31.9).
 constexpr int64_t kSliceTokens = 128;
 
-// Up to this many tokens the down projection runs on down_tokens_kernel (8192 x
-// 8192 at rank 384, the whole call: one token 19.7 us, 21.3 on slices; four
-// 21.8 and 22.1; five 23.8 and 22.3).
+// Up to this many tokens the down projection runs on down_tokens_kernel (the
+// whole call; 8192 x 8192 at rank 384: one token 19.7 us, 21.9 on slices; four
+// 21.2 and 22.1; five 23.8 and 22.3; 4096 x 4096 at rank 64: 8.7 and 11.7, 10.2
+// and 11.8).  Beside a wide product it loses from two tokens on (5120 -> 27648 at
+// rank 384: one token 32.0 and 32.7, two 33.3 and 32.8, four 36.2 and 33.2).
 constexpr int64_t kDownTokens = 4;
 
 // Token tile of the slice kernels.
@@ -1018,8 +1025,13 @@ int launch_slice(bool i8, const CUtensorMap& tmW, const CUtensorMap& tmX, const 
 // slices: few rank rows make few large tiles, so K is split instead.  The
 // product behind it starts at once and takes the SMs that this grid leaves, but
 // its pairs share none with a CTA of this one: where that product's `pairs`
-// leave SMs idle (one wave), P keeps to those if its tiles fit there (1000
-// tokens through 4096 x 4096 at rank 64: 42.2 us, 46.2 with P on 64 SMs).
+// leave SMs idle (one wave), P keeps to those if its tiles fit there.  Measured
+// with P beside the product and with P on more SMs: 1000 tokens through 4096 x
+// 4096 at rank 64, int8 25.6 and 28.9 us, with a checkpoint 39.6 and 46.5; 512
+// through 8192 x 8192 at rank 64 36.2 and 45.3; 257 at rank 384 38.1 and 48.4.
+// The rule asks whether the tiles fit, not how long they take there: where they
+// leave no room to split K the product waits for P (rank 384, 8192 x 8192: 400
+// tokens 74.6 us beside, 49.0 otherwise; 512 with a checkpoint 112 and 81).
 int launch_p_slice(const void* x, const void* A, __nv_bfloat16* P, __nv_bfloat16* P_lo, float s, int64_t tokens,
                    int64_t d_in, int64_t r, long long pairs, const DeviceInfo* dev, cudaStream_t st) {
   const long long spare = dev->num_sms - 2 * std::min<long long>(pairs, dev->pair_clusters);
@@ -1049,9 +1061,11 @@ int launch_p_slice(const void* x, const void* A, __nv_bfloat16* P, __nv_bfloat16
 }
 
 // Tile width of the products with whole accumulators in registers: 128-wide
-// tiles take about 0.58 of a 256-wide one's time (256 tokens through 8192 x 8192
-// in 8 bits: 26 us, 31 on 256-wide tiles that fill 32 of 74 pairs), so the width
-// whose waves over the pairs end first.
+// tiles take about 0.58 of a 256-wide one's time, so the width whose waves over
+// the pairs end first.  In 8 bits: 256 tokens through 8192 x 8192 24.6 us, 29.0 on
+// 256-wide tiles that fill 32 of 74 pairs; 2000 tokens through 4096 x 4096 (four
+// waves or two) 42.6 and 28.6, 4096 tokens (seven or four) 74 to 76 and 54 to 62;
+// with a checkpoint 88 and 60, 149 and 116 to 131.
 int pick_bn_waves(long long tiles_m, long long N, const DeviceInfo* dev) {
   const auto waves = [&](int width) { return cdiv(tiles_m * cdiv(N, width), dev->pair_clusters); };
   return 58 * waves(128) < 100 * waves(256) ? 128 : 256;
@@ -1190,7 +1204,12 @@ namespace {
 // that an SM holds many rows and one's reduction overlaps another's loads: 8192
 // rows of 4096 bf16 with a residual took 39.4 us, 47.4 with 16 columns.  Few
 // rows, and rows of single fp32 values (whose 32 loads a thread are too many),
-// take up to 1024 threads, 8 columns each where that is enough.
+// take up to 1024 threads, 8 columns each where that is enough.  Rows past 8192
+// columns take 1024 threads of 64 registers, which spill in some types, and past
+// 32768 they are read twice; with the reader (dequant_i8_kernel) after them:
+// 8192 x 16384 bf16 with norm, residual and y 242.6 us (its bytes: 246), 8192 x
+// 27648 bf16 268.2 (208), 4096 x 53248 bf16 440.8 (200), 2000 x 16384 fp32 with
+// norm, residual and y 141 (110), 2000 x 16385 fp32 without y 418 (90).
 template <typename T, int VEC, bool HAS_W>
 int launch_rows_i8(const RowsI8Args& a, const DeviceInfo* dev, cudaStream_t st) {
   const long long most = VEC == 1 || a.rows < 2LL * dev->num_sms ? 1024 : 64;
@@ -1255,8 +1274,9 @@ int launch_compose_fwd_ckpt8(const void* base_out, const void* lora_out, const v
   const int threads = static_cast<int>(std::min<long long>(256, align_up(blocks * L::kLanes, 32)));
   const long long gx = cdiv(blocks, threads / L::kLanes);
   // one wave of resident CTAs (two an SM): a CTA starts its loads once and then
-  // keeps the next group's in flight (at 8192 x 8192 bf16 87.6 us; 90.7 with 8
-  // CTAs an SM in turn, 103.6 with 16)
+  // keeps the next group's in flight (8192 x 8192 bf16, while each CTA took a
+  // stretch of rows: 87.6 us, 90.7 with 8 CTAs an SM, 103.6 with 16; with rows in
+  // turn over the grid one wave takes 78)
   const long long gy = std::max<long long>(1, std::min<long long>({2LL * dev->num_sms / gx, cdiv(tokens, kCkptRows), 65535}));
   return launch_after(bias ? compose_fwd_ckpt8_kernel<L, true> : compose_fwd_ckpt8_kernel<L, false>,
                       dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), threads, st,
@@ -1317,7 +1337,8 @@ int dora_dequantize_i8(const int8_t* q, const float* scale, int64_t rows, int64_
     const int threads = static_cast<int>(std::min<long long>(256, align_up(vecs, 32)));
     const long long gx = cdiv(vecs, threads);
     // short CTAs, 32 an SM in all; of the wider single-column ones 8 (2000 x
-    // 4099 fp32: 13.5 us, 17.6 with 32; 8192 x 8192 bf16: 31.7, 34.1 with 8)
+    // 4099 fp32: 13.5 us, 17.6 with 32; 8192 x 8192 bf16: 31.7, 34.1 with 8).  The
+    // former's 41 MB would take 6.3: it moves one byte in and four out an access
     const long long ctas = (vec > 1 ? 32LL : 8LL) * dev->num_sms;
     const long long gy = std::max<long long>(1, std::min<long long>({cdiv(rows, u), 65535, ctas / gx}));
     return launch_after(kernel, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), threads, st, q, scale, rows,

@@ -23,7 +23,7 @@
 // last step overlaps the next tile's first two chunks.  Tiles of 128 columns
 // (four of the warps then only keep step) serve products whose 256-wide tiles
 // leave half of the pairs without one.  Measured: 8192 x 8192 x 8192 at rank
-// 384 in 930 to 990 us with P's launch and the reader's 31 (1.25 TFLOP with P's
+// 384 in 930 to 1030 us with P's launch and the reader's 31 (1.25 TFLOP with P's
 // second half), bound by the tensor cores under the power limit; 1000 x 4096 x
 // 4096 at rank 64 in 35 us, of which the main loop is 20 to 25 and the epilogue
 // 4.2.

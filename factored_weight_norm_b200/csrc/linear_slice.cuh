@@ -11,13 +11,14 @@
 // into its own (the ring is free by then), and each finishes its share of the
 // tokens from all of them.  int32 partial sums are exact in any order; the
 // adapter's product lies wholly in the last split, so its fp32 sum is one
-// CTA's; the fp32 sums of the down projection are added in split order.
+// CTA's; the fp32 sums of the down projection are added in split order, so P's
+// last bits depend on the number of splits, and with it on the batch.
 // The meeting is what costs beyond the stream: it is done once for the whole
 // tile, by all warps, with the loads from all splits in flight together (in
 // two rounds of 64 tokens by four warps, split after split, 128 tokens took 10
 // of 25 us).  Measured at 8192 x 8192 without an adapter: one token 15.2 us (67
 // MB streamed in 10, 6 TB/s or more; 2.5 to the first bytes, 2.5 to join; 0.4 for
-// the proxy fence before them), 128 tokens 20.4.
+// the proxy fence before them), 128 tokens 21.1.
 #pragma once
 
 #include "linear_i8.cuh"

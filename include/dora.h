@@ -325,8 +325,9 @@ DORA_API int dora_fused_linear_fwd(const void* x, const void* W, const void* A, 
  * stretch shorter).  Codes are [rows, cols], row-major, in [-127, 127].  A
  * stretch whose values are all below 2^-100 keeps zeros and the scale 0; one
  * that holds an infinity or a NaN gets the scale NaN, so that all its values
- * come back as NaN.  The pages have no 8-bit form; these calls have no
- * counterpart there. */
+ * come back as NaN.  Outputs overlap neither inputs nor one another, except where
+ * a call says so.  The pages have no 8-bit form; these calls have no counterpart
+ * there. */
 
 /* The 8-bit rows of x (+ residual) without a norm: the input of a projection
  * that follows no norm, or a weight's output channels (quantised once).
