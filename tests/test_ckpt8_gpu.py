@@ -465,3 +465,30 @@ def test_two_graphs_share_a_workspace():
             call() if turn == 3 else graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, ref)), turn
+
+
+@pytest.mark.parametrize("dtype, d", [(BF, 520), (F32, 263)])
+def test_a_checkpoint_rewritten_under_dependent_launches(dtype, d):
+    # forward and backward over the same small buffers, magnitudes changed in place between them
+    T, turns = 200, 60
+    sets = [_acts(T, d, dtype, False, seed=40 + i) for i in range(4)]
+    fresh = []
+    for base, lora, m, n, _, dy in sets:
+        y, z8, zs = D.dora_compose_fwd_ckpt8(base, lora, m, n, 0.5)
+        fresh.append((y, z8, zs, *D.dora_compose_bwd_ckpt8(dy, z8, zs, m, n, 0.5)))
+        torch.cuda.synchronize()
+    cur = [torch.empty_like(t) for t in (sets[0][0], sets[0][1], sets[0][2], sets[0][3], sets[0][5])]
+    out = [torch.empty_like(t) for t in fresh[0]]
+    ws = torch.empty(D.dora_compose_bwd_ckpt8_workspace_size(T, d), dtype=torch.uint8, device=DEV)
+    got = [[torch.empty_like(t) for t in fresh[0]] for _ in range(turns)]
+    for i in range(turns):
+        base, lora, m, n, _, dy = sets[i % 4]
+        for dst, src in zip(cur, (base, lora, m, n, dy)):
+            dst.copy_(src)
+        D.dora_compose_fwd_ckpt8(*cur[:4], 0.5, *out[:3])
+        D.dora_compose_bwd_ckpt8(cur[4], out[1], out[2], cur[2], cur[3], 0.5, *out[3:], workspace=ws)
+        for dst, src in zip(got[i], out):
+            dst.copy_(src)
+    torch.cuda.synchronize()
+    for i, row in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(row, fresh[i % 4])), i

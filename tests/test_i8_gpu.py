@@ -618,3 +618,54 @@ def test_serving_a_module_with_the_norm_of_its_codes(T):
     exact = oracle.row_norm(kept, P.f64(A), P.f64(B), s)
     slack = U * np.linalg.norm(kept, axis=1) + P.NORM_RTOL_BF16 * exact
     assert np.all(np.abs(P.f64(n) - exact) <= slack)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_buffers_rewritten_under_dependent_launches(captured):
+    # every call starts under the one before it, which has just rewritten what it
+    # reads: the same small buffers over and over, so that the lines which an SM
+    # read last time would still be in its cache
+    T, d, N, turns = 160, 512, 136, 60
+    xs = [_rows(T, d, BF, 140 + i) * 2.0 ** (i % 5) for i in range(4)]
+    w = torch.ones(d, dtype=BF, device=DEV)
+    k = _module(T, d, N, 0, seed=139)
+    x, q, sc = torch.empty_like(xs[0]), torch.empty(T, d, dtype=torch.int8, device=DEV), torch.empty(T, device=DEV)
+    val, out = torch.empty_like(x), torch.empty(T, N, dtype=BF, device=DEV)
+    small = torch.empty(64, N, dtype=BF, device=DEV)
+    want = []
+    for t in xs:
+        a, b, _, _ = D.dora_rms_norm_i8(t, w)
+        torch.cuda.synchronize()
+        lin = {**k, "x_q": a, "x_scale": b}
+        part = {**k, "x_q": a[:64].clone(), "x_scale": b[:64].clone()}
+        want.append([D.dora_dequantize_i8(a, b), D.dora_linear_i8_fwd(**lin), D.dora_linear_i8_fwd(**part)])
+        torch.cuda.synchronize()
+    got = [[torch.empty_like(t) for t in want[0]] for _ in range(turns)]
+
+    def chain():
+        for i in range(turns):
+            x.copy_(xs[i % 4])
+            D.dora_rms_norm_i8(x, w, q=q, scale=sc)
+            D.dora_dequantize_i8(q, sc, out=val)
+            D.dora_linear_i8_fwd(**{**k, "x_q": q, "x_scale": sc}, y=out)
+            D.dora_linear_i8_fwd(**{**k, "x_q": q[:64], "x_scale": sc[:64]}, y=small)
+            D.dora_quantize_rows_i8(val, q=q, scale=sc)  # rewritten at once
+            for dst, src in zip(got[i], (val, out, small)):
+                dst.copy_(src)
+
+    if captured:
+        chain()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain()
+        for row in got:
+            for t in row:
+                t.fill_(7.0)
+        graph.replay()
+    else:
+        chain()
+    torch.cuda.synchronize()
+    assert D.dora_device_status() == D.DORA_OK
+    for i, row in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(row, want[i % 4])), i
